@@ -61,6 +61,9 @@ SIGNATURES = {
                            _i, _i, _f, _i, _vp, _sz, _vp], _i),
     "fa_bwd_f32_packed": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i,
                            _i, _i, _i, _i, _f, _i, _vp, _sz, _vp], _i),
+    "fa_doc_ranges": ([_vp, _vp, _vp, _i, _i, _vp], _i),
+    "fa_fwd_mod": ([_vp] * 9 + [_i] * 6 + [_f, _i, _f, _vp], _i),
+    "fa_bwd_mod": ([_vp] * 13 + [_i] * 6 + [_f, _i, _f, _vp, _sz, _vp], _i),
     "fa_merge": ([_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp], _i),
     "fa_accumulate": ([_vp, _vp, _vp, _sz, _vp], _i),
     "fa_selftest_timeout": ([ctypes.c_longlong, _vp], _i),
@@ -436,6 +439,130 @@ def bwd_packed(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tenso
                                   int(bool(causal)), _ptr(workspace), ws_bytes,
                                   _stream_handle(stream))
     _check(name, st)
+    return dQ, dK, dV
+
+
+def _check_vec(name: str, t: Optional[torch.Tensor], shape, dtype, device) -> None:
+    if t is None:
+        return
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on the inputs' CUDA device")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def _check_device(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on the inputs' device ({device}), not {t.device}")
+
+
+def doc_ranges(doc_ids: torch.Tensor, starts: Optional[torch.Tensor] = None,
+               ends: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None):
+    """The documents of a batch as ``fwd_mod`` and ``bwd_mod`` take them, through
+    ``fa_doc_ranges``: doc_ids [B, N] int32 (an id per key token, negative for padding)
+    -> (starts, ends), [B, N] int32 each, the run of equal ids every token lies in.  One
+    call serves every layer's forward and backward calls over the batch."""
+    if doc_ids.dim() != 2:
+        raise ValueError("doc_ids must have two dimensions [B, N]")
+    B, N = doc_ids.shape
+    _check_bhnd("doc_ids", doc_ids, (B, N), torch.int32)
+    starts = torch.empty_like(doc_ids) if starts is None else starts
+    ends = torch.empty_like(doc_ids) if ends is None else ends
+    _check_vec("starts", starts, (B, N), torch.int32, doc_ids.device)
+    _check_vec("ends", ends, (B, N), torch.int32, doc_ids.device)
+    with torch.cuda.device(doc_ids.device):
+        st = lib().fa_doc_ranges(_ptr(doc_ids), _ptr(starts), _ptr(ends), B, N,
+                                 _stream_handle(stream))
+    _check("fa_doc_ranges", st)
+    return starts, ends
+
+
+def _mod_shapes(Q, K, V, slopes, prefix, docs):
+    if Q.dim() != 4 or K.dim() != 4:
+        raise ValueError("Q must be [B, H, Nq, d] and K, V [B, Hkv, Nk, d]")
+    B, H, Nq, d = Q.shape
+    Hkv, Nk = K.shape[1], K.shape[2]
+    _check_bhnd("Q", Q, (B, H, Nq, d), torch.bfloat16)
+    for name, t in (("K", K), ("V", V)):
+        _check_bhnd(name, t, (B, Hkv, Nk, d), torch.bfloat16)
+    _check_device(Q.device, K=K, V=V)
+    _check_vec("slopes", slopes, (H,), torch.float32, Q.device)
+    _check_vec("prefix", prefix, (B,), torch.int32, Q.device)
+    starts, ends = (None, None) if docs is None else docs
+    _check_vec("docs[0]", starts, (B, Nk), torch.int32, Q.device)
+    _check_vec("docs[1]", ends, (B, Nk), torch.int32, Q.device)
+    mods = (_ptr(slopes), _ptr(prefix), _ptr(starts), _ptr(ends))
+    return B, H, Hkv, Nq, Nk, d, mods
+
+
+def fwd_mod(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: Optional[float] = None,
+            causal: bool = False, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+            prefix: Optional[torch.Tensor] = None, docs=None, O: Optional[torch.Tensor] = None,
+            LSE: Optional[torch.Tensor] = None, want_lse: bool = True,
+            stream: Optional[torch.cuda.Stream] = None):
+    """Forward with modified scores and shared key heads through ``fa_fwd_mod`` (bf16).
+
+    Q [B, H, Nq, d]; K, V [B, Hkv, Nk, d], H a multiple of Hkv; the queries are the last
+    Nq of the Nk tokens, row i at position p = i + Nk - Nq.  ``softcap`` c > 0 turns the
+    scaled score z into c tanh(z / c); ``slopes`` [H] float32 subtracts slopes[h] |p - j|;
+    ``causal`` hides keys past p except the first ``prefix`` [B] int32 of each sequence;
+    ``docs`` = ``doc_ranges(ids)`` hides keys of other documents.  A row that sees no key
+    gets O = 0 and LSE = -inf.  Returns (O, LSE); LSE is None when ``want_lse`` is False
+    and none is passed."""
+    B, H, Hkv, Nq, Nk, d, mods = _mod_shapes(Q, K, V, slopes, prefix, docs)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    O = torch.empty_like(Q) if O is None else O
+    _check_bhnd("O", O, (B, H, Nq, d), torch.bfloat16)
+    if LSE is None and want_lse:
+        LSE = torch.empty((B, H, Nq), device=Q.device, dtype=torch.float32)
+    _check_vec("LSE", LSE, (B, H, Nq), torch.float32, Q.device)
+    _check_device(Q.device, O=O)
+    with torch.cuda.device(Q.device):
+        st = lib().fa_fwd_mod(_ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(LSE), *mods, B, H, Hkv,
+                              Nq, Nk, d, float(scale), int(bool(causal)), float(softcap),
+                              _stream_handle(stream))
+    _check("fa_fwd_mod", st)
+    return O, LSE
+
+
+def bwd_mod(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tensor,
+            dO: torch.Tensor, LSE: torch.Tensor, scale: Optional[float] = None,
+            causal: bool = False, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+            prefix: Optional[torch.Tensor] = None, docs=None,
+            dQ: Optional[torch.Tensor] = None, dK: Optional[torch.Tensor] = None,
+            dV: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+            stream: Optional[torch.cuda.Stream] = None):
+    """Backward of ``fwd_mod`` with the same modifications through ``fa_bwd_mod``.  dK and
+    dV [B, Hkv, Nk, d] are summed over the query heads that share a key head; slopes are
+    constants.  Every row of every gradient is written.  Returns (dQ, dK, dV)."""
+    B, H, Hkv, Nq, Nk, d, mods = _mod_shapes(Q, K, V, slopes, prefix, docs)
+    for name, t in (("O", O), ("dO", dO)):
+        _check_bhnd(name, t, (B, H, Nq, d), torch.bfloat16)
+    _check_bhnd("LSE", LSE, (B, H, Nq), torch.float32)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    dQ = torch.empty_like(Q) if dQ is None else dQ
+    dK = torch.empty_like(K) if dK is None else dK
+    dV = torch.empty_like(V) if dV is None else dV
+    _check_bhnd("dQ", dQ, (B, H, Nq, d), torch.bfloat16)
+    for name, t in (("dK", dK), ("dV", dV)):
+        _check_bhnd(name, t, (B, Hkv, Nk, d), torch.bfloat16)
+    if workspace is None:
+        workspace = torch.empty(max(workspace_bytes(B, H, Nq, d), 16), device=Q.device,
+                                dtype=torch.uint8)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _check_device(Q.device, O=O, dO=dO, LSE=LSE, dQ=dQ, dK=dK, dV=dV, workspace=workspace)
+    ws_bytes = workspace.numel() * workspace.element_size()
+    with torch.cuda.device(Q.device):
+        st = lib().fa_bwd_mod(_ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(dO), _ptr(LSE), _ptr(dQ),
+                              _ptr(dK), _ptr(dV), *mods, B, H, Hkv, Nq, Nk, d, float(scale),
+                              int(bool(causal)), float(softcap), _ptr(workspace), ws_bytes,
+                              _stream_handle(stream))
+    _check("fa_bwd_mod", st)
     return dQ, dK, dV
 
 

@@ -48,6 +48,7 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "mod.cuh"
 #include "sm100.cuh"
 
 namespace fa {
@@ -77,7 +78,6 @@ __device__ __forceinline__ uint32_t split_operand_col(uint32_t base, int kk) {
   return base + (kk / 4) * 64 + (kk % 4) * 8;
 }
 constexpr uint32_t kTmemCols = 512;
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct BwdArgs {
   unsigned int* err;
@@ -104,6 +104,7 @@ struct BwdArgs {
   int dq_aligned32;  // dQ starts on a 32-byte boundary (its rows then allow 32-byte stores)
   float scale;
   float scale_log2;
+  ModArgs mod;  // modified-score calls only
 };
 
 // Head bh's sequence: its query and key row counts (Nq, Nk, or its entries of
@@ -292,7 +293,7 @@ struct DkdvLayout {
   static_assert(kAlloc <= 232448, "shared memory over the 227 KB per-block limit");
 };
 
-template <int D>
+template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -355,7 +356,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tdV = tmem, tdK = tmem + D, tS = tmem + 2 * D, tdP = tmem + 2 * D + 128;
 
   // unit w: key tile j of head bh, meeting query tiles i0 .. i0 + m - 1 of its sequence
-  // (m = 0: the tile lies past the sequence's keys, or the sequence has no queries)
+  // (m = 0: the tile lies past the sequence's keys, or the sequence has no queries).
+  // Modified scores: bh is a head of K and V, and its query heads follow one another, m /
+  // group tiles each; the products of all of them add up in the same accumulators.
   auto unit = [&](int w, int& bh, int& j, int& i0, int& m, int& lk, int& off, int& tq0,
                   int& tk0, int& lq) {
     if (args.causal) {
@@ -368,6 +371,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     seq_info(args, bh, lq, lk, tq0, tk0);
     off = lk - lq;  // position of query row 0 among the keys
     i0 = 0;
+    if constexpr (kMode != kModNone) {
+      const int b = bh / args.mod.Hkv;
+      const int last = min(j * kTile + kTile, lk) - 1;
+      const int q_lo = mod_key(args.mod, b, j * kTile, off, lq, lk, args.causal).lo;
+      const int q_hi = mod_key(args.mod, b, last, off, lq, lk, args.causal).hi;
+      i0 = q_lo / kTile;
+      m = q_hi > q_lo ? ((q_hi + kTile - 1) / kTile - i0) * args.mod.group : 0;
+      return;
+    }
     if (j * kTile >= lk || lq == 0) {
       m = 0;
       return;
@@ -375,6 +387,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // causal: first query tile with a row whose position reaches key j*128
     if (args.causal && j * kTile > off) i0 = (j * kTile - off) / kTile;
     m = (lq + kTile - 1) / kTile - i0;
+  };
+  // query tile t of the unit: tile i of query head bhq
+  auto q_tile = [&](int bh, int i0, int m, int t, int& bhq, int& i) {
+    bhq = bh;
+    i = i0 + t;
+    if constexpr (kMode != kModNone) {
+      const int per = m / args.mod.group;
+      const int g = t / per;
+      bhq = bh * args.mod.group + g;
+      i = i0 + t - g * per;
+    }
   };
   auto qslot = [&](int s) -> uint32_t { return base + L::kQ0 + s * L::kTileBytes; };
   auto doslot = [&](int s) -> uint32_t { return base + L::kDO0 + s * L::kDOSlotBytes; };
@@ -404,13 +427,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                           tma_y(bh, j * kTile), tma_z(bh, tk0, j * kTile));
       }
       ++kv_loads;
-      for (int i = i0; ok && i < i0 + m; ++i) {
+      for (int t = 0; ok && t < m; ++t) {
+        int bhq, i;
+        q_tile(bh, i0, m, t, bhq, i);
         ok = wait_warp(bar(L::kBarQEmpty + qs), qph ^ 1);
         if (!ok) break;
         mbar_arrive_expect_tx_elect(bar(L::kBarQFull + qs), L::kTileBytes);
         for (int c = 0; c < D / 64; ++c)
           tma_load_3d_elect(qslot(qs) + c * L::kBoxBytes, &tmQ, bar(L::kBarQFull + qs), c * 64,
-                            tma_y(bh, i * kTile), tma_z(bh, tq0, i * kTile));
+                            tma_y(bhq, i * kTile), tma_z(bhq, tq0, i * kTile));
         q_issued[qs] = 1;
         q_phase[qs] = qph;
         if (++qs == L::kQStages) qs = 0, qph ^= 1;
@@ -420,9 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx_elect(fb, L::kTileBytes + 1024);
         for (int c = 0; c < D / 64; ++c)
           tma_load_3d_elect(doslot(ds) + c * L::kBoxBytes, &tmdO, fb, c * 64,
-                            tma_y(bh, i * kTile), tma_z(bh, tq0, i * kTile));
-        tma_load_3d_elect(doslot(ds) + L::kSlotL, &tmL2, fb, i * kTile, bh, 0);
-        tma_load_3d_elect(doslot(ds) + L::kSlotD, &tmD, fb, i * kTile, bh, 0);
+                            tma_y(bhq, i * kTile), tma_z(bhq, tq0, i * kTile));
+        tma_load_3d_elect(doslot(ds) + L::kSlotL, &tmL2, fb, i * kTile, bhq, 0);
+        tma_load_3d_elect(doslot(ds) + L::kSlotD, &tmD, fb, i * kTile, bhq, 0);
         d_issued[ds] = 1;
         d_phase[ds] = dph;
         if (++ds == L::kDOStages) ds = 0, dph ^= 1;
@@ -571,10 +596,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       unit(w, bh, j, i0, m, lk, off, tq0, tk0, lq);
       live = m > 0;
       if (!live) {
-        // a sequence with keys but no queries: no query sees these keys, so their
-        // gradients are exactly zero (group g writes its half of each row)
+        // a sequence with keys but no queries (modified scores: keys that every mask
+        // hides): no query sees these keys, so their gradients are exactly zero (group g
+        // writes its half of each row)
         const int kv_row = j * kTile + row;
-        if (lq == 0 && kv_row < lk) {
+        if ((kMode != kModNone || lq == 0) && kv_row < lk) {
           const size_t orow = k_row_offset(args, bh, tk0, kv_row, D) + g * (D / 2);
           uint4* zk = reinterpret_cast<uint4*>(args.dK + orow);
           uint4* zv = reinterpret_cast<uint4*>(args.dV + orow);
@@ -586,7 +612,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      for (int i = i0; i < i0 + m; ++i) {
+      // modified scores: the queries that see this thread's key, those that see every key
+      // of the tile
+      RowLimits lim_row{0, 0};
+      int full_lo = 0, full_hi = 0;
+      if constexpr (kMode != kModNone) {
+        const int b = bh / args.mod.Hkv;
+        const int first = j * kTile, last = min(first + kTile, lk) - 1;
+        lim_row = mod_key(args.mod, b, min(first + row, last), off, lq, lk, args.causal);
+        full_lo = mod_key(args.mod, b, last, off, lq, lk, args.causal).lo;
+        full_hi = mod_key(args.mod, b, first, off, lq, lk, args.causal).hi;
+      }
+      for (int t = 0; t < m; ++t) {
+        int bhq, i;
+        q_tile(bh, i0, m, t, bhq, i);
         // this tile's L2 and D rows sit in its dO slot
         const uint8_t* sb = smem + L::kDO0 + stage * L::kDOSlotBytes;
         const float* sL = reinterpret_cast<const float*>(sb + L::kSlotL) + col0;
@@ -607,27 +646,72 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int delta = (j - i) * kTile - off;
           const bool diag = args.causal && delta > -kTile;
           const uint64_t scale2 = f32x2(args.scale_log2, args.scale_log2);
+          const float unit = kMode == kModCap ? args.mod.cap_log2 : args.scale_log2;
+          const uint64_t unit2 = f32x2(unit, unit);
+          bool masked = false, straddles = false;
+          int mlo = 0;
+          unsigned width = 0;
+          float sl = 0.f, pos_d = 0.f;  // bias of column c: sl * (pos_d + c)
+          if constexpr (kMode != kModNone) {
+            masked = i * kTile + col0 < full_lo || i * kTile + col0 + kCols > full_hi;
+            mlo = lim_row.lo - i * kTile - col0;
+            width = static_cast<unsigned>(lim_row.hi - lim_row.lo);
+            if (args.mod.slopes != nullptr) {
+              // -slope |p - y|, y this thread's key, p = i*128 + off + column
+              sl = -args.mod.slopes[bhq % args.H] * kLog2e;
+              const int p0 = i * kTile + col0 + off;  // position of the group's column 0
+              pos_d = static_cast<float>(p0 - (j * kTile + row));
+              const bool before = p0 >= j * kTile + kTile - 1;      // keys before queries
+              const bool after = p0 + kCols - 1 <= j * kTile;       // keys after queries
+              straddles = !before && !after;
+              if (after && !before) sl = -sl;
+            }
+          }
           // the group's 64 columns in two halves of 32; each half's bf16 P^T is stored and
           // announced as soon as it is made
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
+            uint32_t pk[kCols / 4];
+            float th[kCols / 2];  // with a cap: tanh of this half's scores
+            if constexpr (kMode == kModCap) {
+#pragma unroll
+              for (int c = 0; c < kCols / 2; ++c)
+                th[c] = __uint_as_float(r[hf * (kCols / 2) + c]);
+              tanh_scores<kCols / 2>(th, args.mod);
+            }
 #pragma unroll
             for (int c = hf * (kCols / 2); c < (hf + 1) * (kCols / 2); c += 2) {
               // x = S^T * scale * log2e - L2 for two query columns in one packed FMA
               const uint64_t nl = *reinterpret_cast<const uint64_t*>(sL + c);
-              const uint64_t x2 =
-                  fma_x2(f32x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), scale2, nl);
               float e0, e1;
-              exp2_pair(x2, e0, e1);
-              if (diag && col0 + c < row + delta) e0 = 0.f;
-              if (diag && col0 + c + 1 < row + delta) e1 = 0.f;
-              p[c] = e0;
-              p[c + 1] = e1;
+              if constexpr (kMode == kModNone) {
+                const uint64_t x2 =
+                    fma_x2(f32x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), scale2, nl);
+                exp2_pair(x2, e0, e1);
+                if (diag && col0 + c < row + delta) e0 = 0.f;
+                if (diag && col0 + c + 1 < row + delta) e1 = 0.f;
+                p[c] = e0;
+                p[c + 1] = e1;
+              } else {
+                float g0, g1;
+                const int k = c - hf * (kCols / 2);
+                mod_prob_pair<kMode>(kMode == kModCap ? th[k] : __uint_as_float(r[c]),
+                                     kMode == kModCap ? th[k + 1] : __uint_as_float(r[c + 1]),
+                                     args.mod, unit2, nl, sl, pos_d + static_cast<float>(c), straddles,
+                                     e0, e1, g0, g1);
+                if (masked && static_cast<unsigned>(c - mlo) >= width) e0 = 0.f;
+                if (masked && static_cast<unsigned>(c + 1 - mlo) >= width) e1 = 0.f;
+                pk[k / 2] = pack_bf16x2(e0, e1);
+                // dS carries the cap's derivative
+                p[c] = kMode == kModCap ? e0 * g0 : e0;
+                p[c + 1] = kMode == kModCap ? e1 * g1 : e1;
+              }
             }
-            uint32_t pk[kCols / 4];
+            if constexpr (kMode == kModNone) {
 #pragma unroll
-            for (int c = 0; c < kCols / 4; ++c)
-              pk[c] = pack_bf16x2(p[hf * (kCols / 2) + 2 * c], p[hf * (kCols / 2) + 2 * c + 1]);
+              for (int c = 0; c < kCols / 4; ++c)
+                pk[c] = pack_bf16x2(p[hf * (kCols / 2) + 2 * c], p[hf * (kCols / 2) + 2 * c + 1]);
+            }
             tmem_st16(tS + lane_off + col0 + hf * (kCols / 4), pk);
             tmem_wait_st();
             warp_arrive(bar(hf == 0 ? L::kBarPReady : L::kBarPReadyB));
@@ -767,7 +851,7 @@ struct DqLayout {
   static_assert(kAlloc <= 232448, "shared memory over the 227 KB per-block limit");
 };
 
-template <int D>
+template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -831,10 +915,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tdQ = tmem, tS = tmem + 128, tdP = tmem + 256, tQt = tmem + 384,
                  tdOt = tmem + 384 + D / 2;
 
-  // unit w: query tile i of head bh, meeting key tiles 0 .. m - 1 of its sequence
-  // (m = 0: the tile lies past the sequence's queries, or the sequence has no keys)
-  auto unit = [&](int w, int& bh, int& i, int& m, int& lq, int& lk, int& off, int& tq0,
+  // head of K and V that query head bh reads
+  auto kv_head = [&](int bh) {
+    if constexpr (kMode != kModNone)
+      return bh / args.H * args.mod.Hkv + bh % args.H / args.mod.group;
+    return bh;
+  };
+  // unit w: query tile i of head bh, meeting key tiles jb .. jb + m - 1 of its sequence
+  // (m = 0: the tile lies past the sequence's queries, or the sequence has no keys; jb is
+  // 0 except for modified scores)
+  auto unit = [&](int w, int& bh, int& i, int& jb, int& m, int& lq, int& lk, int& off, int& tq0,
                   int& tk0) {
+    jb = 0;
     if (args.causal) {
       i = args.n_qt - 1 - w / args.BH;  // last query tile meets the most key tiles
       bh = w % args.BH;
@@ -844,6 +936,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     seq_info(args, bh, lq, lk, tq0, tk0);
     off = lk - lq;
+    if constexpr (kMode != kModNone) {
+      const int b = bh / args.H;
+      const int last = min(i * kTile + kTile, lq) - 1;
+      const int lo = mod_row(args.mod, b, i * kTile, off, lk, args.causal).lo;
+      const int hi = mod_row(args.mod, b, last, off, lk, args.causal).hi;
+      jb = lo / kTile;
+      m = hi > lo ? (hi + kTile - 1) / kTile - jb : 0;
+      return;
+    }
     if (i * kTile >= lq || lk == 0) {
       m = 0;
       return;
@@ -865,8 +966,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int live = 0;  // 1 when the unit just processed had work: units counts only those
       for (int r = 0, w = snake_unit(0); ok && w < args.total_units;
          w = snake_unit(++r), units += live) {
-        int bh, i, m, lq, lk, off, tq0, tk0;
-        unit(w, bh, i, m, lq, lk, off, tq0, tk0);
+        int bh, i, jb, m, lq, lk, off, tq0, tk0;
+        unit(w, bh, i, jb, m, lq, lk, off, tq0, tk0);
         live = m > 0;
         if (!live) continue;
         if (units > 0) ok = wait_warp(bar(L::kBarQEmpty), (units - 1) & 1);
@@ -879,14 +980,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tma_y(bh, i * kTile), tma_z(bh, tq0, i * kTile));
         }
         ++q_loads;
-        for (int j = 0; ok && j < m; ++j) {
+        const int kbh = kv_head(bh);
+        for (int j = jb; ok && j < jb + m; ++j) {
           ok = wait_warp(bar(L::kBarKEmpty + ks), kph ^ 1);
           if (!ok) break;
           mbar_arrive_expect_tx_elect(bar(L::kBarKFull + ks), L::kTileBytes);
           for (int c = 0; c < D / 64; ++c)
             tma_load_3d_elect(base + L::kK0 + ks * L::kTileBytes + c * L::kBoxBytes, &tmK,
-                              bar(L::kBarKFull + ks), c * 64, tma_y(bh, j * kTile),
-                              tma_z(bh, tk0, j * kTile));
+                              bar(L::kBarKFull + ks), c * 64, tma_y(kbh, j * kTile),
+                              tma_z(kbh, tk0, j * kTile));
           k_issued[ks] = 1;
           k_phase[ks] = kph;
           if (++ks == L::kKStages) ks = 0, kph ^= 1;
@@ -895,8 +997,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx_elect(bar(L::kBarVFull + vs), L::kTileBytes);
           for (int c = 0; c < D / 64; ++c)
             tma_load_3d_elect(base + L::kV0 + vs * L::kTileBytes + c * L::kBoxBytes, &tmV,
-                              bar(L::kBarVFull + vs), c * 64, tma_y(bh, j * kTile),
-                              tma_z(bh, tk0, j * kTile));
+                              bar(L::kBarVFull + vs), c * 64, tma_y(kbh, j * kTile),
+                              tma_z(kbh, tk0, j * kTile));
           v_issued[vs] = 1;
           v_phase[vs] = vph;
           if (++vs == L::kVStages) vs = 0, vph ^= 1;
@@ -945,8 +1047,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int live = 0;
       for (int r = 0, w = snake_unit(0); ok && w < args.total_units;
          w = snake_unit(++r), units += live) {
-        int bh, i, m, lq, lk, off, tq0, tk0;
-        unit(w, bh, i, m, lq, lk, off, tq0, tk0);
+        int bh, i, jb, m, lq, lk, off, tq0, tk0;
+        unit(w, bh, i, jb, m, lq, lk, off, tq0, tk0);
         live = m > 0;
         if (!live) continue;
         ok = wait_warp(bar(L::kBarQTmem), units & 1);
@@ -1014,10 +1116,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     int live = 0;
     for (int r = 0, w = snake_unit(0); ok && w < args.total_units;
          w = snake_unit(++r), units += live) {
-      int bh, i, m, lq, lk, off, tq0, tk0;
-      unit(w, bh, i, m, lq, lk, off, tq0, tk0);
+      int bh, i, jb, m, lq, lk, off, tq0, tk0;
+      unit(w, bh, i, jb, m, lq, lk, off, tq0, tk0);
       live = m > 0;
-      if (!live) continue;
+      if (!live) {
+        if constexpr (kMode != kModNone) {
+          // rows that see no key have no gradient (group g writes its half of each row)
+          if (i * kTile + row < lq) {
+            uint4* z = reinterpret_cast<uint4*>(
+                args.dQ + q_row_offset(args, bh, tq0, i * kTile + row, D) + g * (D / 2));
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) z[c] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        continue;
+      }
       // This unit's Q and dO rows into tensor memory: thread = query row = TMEM lane;
       // group g copies the d-columns [g*D/2, (g+1)*D/2), one 32-bit column per pair of
       // bf16 elements.  The tiles sit in shared memory as 64-column boxes with the
@@ -1053,7 +1166,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t prow = static_cast<size_t>(bh) * args.Npad + q_row;  // q_row < Npad
       const float nl2row = args.L2pad[prow];   // -LSE * log2(e) of this query row
       const float ndrow = args.Dpad[prow];     // -D of this query row
-      for (int j = 0; j < m; ++j) {
+      // modified scores: this row's visible keys, the keys that every row of the tile sees
+      RowLimits lim_row{0, 0};
+      int full_lo = 0, full_hi = 0;
+      float slope2 = 0.f;
+      if constexpr (kMode != kModNone) {
+        const int b = bh / args.H;
+        const int first = i * kTile, last = min(first + kTile, lq) - 1;
+        lim_row = mod_row(args.mod, b, min(q_row, last), off, lk, args.causal);
+        full_lo = mod_row(args.mod, b, last, off, lk, args.causal).lo;
+        full_hi = mod_row(args.mod, b, first, off, lk, args.causal).hi;
+        if (args.mod.slopes != nullptr) slope2 = args.mod.slopes[bh % args.H] * kLog2e;
+      }
+      for (int j = jb; j < jb + m; ++j) {
         ok = wait_warp(bar(L::kBarSFull), s_cnt & 1);
         if (!ok) break;
         ++s_cnt;
@@ -1074,6 +1199,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int lim = args.causal ? min(lk, q_row + off + 1) : lk;
           const uint64_t scale2 = f32x2(args.scale_log2, args.scale_log2);
           const uint64_t nl2 = f32x2(nl2row, nl2row);
+          if constexpr (kMode != kModNone) {
+            const bool masked = kv0 < full_lo || kv0 + kCols > full_hi;
+            const int mlo = lim_row.lo - kv0;
+            const unsigned width = static_cast<unsigned>(lim_row.hi - lim_row.lo);
+            // -slope |p - j| = sl (pos_d + c) before the tile's straddling keys are seen to
+            const int pos0 = i * kTile + off;
+            const bool before = kv0 + kCols - 1 <= pos0, after = kv0 >= pos0 + kTile - 1;
+            const float sl = before ? slope2 : -slope2;
+            const float pos_d = static_cast<float>(kv0 - (q_row + off));
+            const float unit = kMode == kModCap ? args.mod.cap_log2 : args.scale_log2;
+            const uint64_t unit2 = f32x2(unit, unit);
+            float x[kCols];
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) x[c] = __uint_as_float(r[c]);
+            if constexpr (kMode == kModCap) tanh_scores<kCols>(x, args.mod);
+#pragma unroll
+            for (int c = 0; c < kCols; c += 2) {
+              float e0, e1, g0, g1;
+              mod_prob_pair<kMode>(x[c], x[c + 1], args.mod, unit2, nl2, sl, pos_d + static_cast<float>(c),
+                                   !before && !after, e0, e1, g0, g1);
+              if (masked && static_cast<unsigned>(c - mlo) >= width) e0 = 0.f;
+              if (masked && static_cast<unsigned>(c + 1 - mlo) >= width) e1 = 0.f;
+              p[c] = kMode == kModCap ? e0 * g0 : e0;
+              p[c + 1] = kMode == kModCap ? e1 * g1 : e1;
+            }
+          } else {
 #pragma unroll
           for (int c = 0; c < kCols; c += 2) {
             const uint64_t x2 =
@@ -1084,6 +1235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (need_mask && kv0 + c + 1 >= lim) e1 = 0.f;
             p[c] = e0;
             p[c + 1] = e1;
+          }
           }
         }
         ok = wait_warp(bar(L::kBarDPFull), dp_cnt & 1);
@@ -1146,7 +1298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ host side
-template <int D>
+template <int D, int kMode>
 cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                      const CUtensorMap& tmdO, const CUtensorMap& tmL2, const CUtensorMap& tmD,
                      const CUtensorMap& tmdK, const CUtensorMap& tmdV, const void* O, const void* dO, const float* LSE, void* dQ, void* dK,
@@ -1173,6 +1325,7 @@ cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   a.dq_aligned32 = (reinterpret_cast<uintptr_t>(dQ) & 31u) == 0;
   a.scale = p.scale;
   a.scale_log2 = p.scale * kLog2e;
+  a.mod = mod_args(p);
   float* Dpad = ws;
   float* L2pad = ws + static_cast<size_t>(p.BH) * a.Npad;
   a.Dpad = Dpad;
@@ -1190,29 +1343,30 @@ cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   if ((e = trace_mark(p, 1, stream)) != cudaSuccess) return e;
 
   BwdArgs a_kv = a, a_q = a;
-  a_kv.total_units = p.BH * a.n_kt;
+  if constexpr (kMode != kModNone) a_kv.BH = p.BH / a.mod.group;  // heads of K and V
+  a_kv.total_units = a_kv.BH * a.n_kt;
   a_q.total_units = p.BH * a.n_qt;
   const int grid_kv = a_kv.total_units < num_sms ? a_kv.total_units : num_sms;
   const int grid_q = a_q.total_units < num_sms ? a_q.total_units : num_sms;
   // the in-kernel register split assumes exactly kRegsLaunch registers a thread at launch
   cudaFuncAttributes fattr;
-  e = cudaFuncGetAttributes(&fattr, bwd_dkdv_kernel<D>);
+  e = cudaFuncGetAttributes(&fattr, bwd_dkdv_kernel<D, kMode>);
   if (e != cudaSuccess) return e;
   if (fattr.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-  e = cudaFuncGetAttributes(&fattr, bwd_dq_kernel<D>);
+  e = cudaFuncGetAttributes(&fattr, bwd_dq_kernel<D, kMode>);
   if (e != cudaSuccess) return e;
   if (fattr.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(bwd_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  e = cudaFuncSetAttribute(bwd_dkdv_kernel<D, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            DkdvLayout<D>::kAlloc);
   if (e != cudaSuccess) return e;
-  bwd_dkdv_kernel<D><<<grid_kv, kThreads, DkdvLayout<D>::kAlloc, stream>>>(
+  bwd_dkdv_kernel<D, kMode><<<grid_kv, kThreads, DkdvLayout<D>::kAlloc, stream>>>(
       tmQ, tmK, tmV, tmdO, tmL2, tmD, tmdK, tmdV, a_kv);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = trace_mark(p, 2, stream)) != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(bwd_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  e = cudaFuncSetAttribute(bwd_dq_kernel<D, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            DqLayout<D>::kAlloc);
   if (e != cudaSuccess) return e;
-  bwd_dq_kernel<D><<<grid_q, kThreads, DqLayout<D>::kAlloc, stream>>>(tmQ, tmK, tmV, tmdO, a_q);
+  bwd_dq_kernel<D, kMode><<<grid_q, kThreads, DqLayout<D>::kAlloc, stream>>>(tmQ, tmK, tmV, tmdO, a_q);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return trace_mark(p, 3, stream);
 }
@@ -1228,11 +1382,18 @@ cudaError_t launch_bwd_sm100(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                              const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
                              float* workspace, const Problem& p, int num_sms,
                              cudaStream_t stream) {
+  auto launch = [&](auto* kernels) {
+    return kernels(tmQ, tmK, tmV, tmdO, tmL2, tmD, tmdK, tmdV, O, dO, LSE, dQ, dK, dV, workspace,
+                   p, num_sms, stream);
+  };
+  const int mode = mod_mode(p);
   if (p.d == 64)
-    return launch_d<64>(tmQ, tmK, tmV, tmdO, tmL2, tmD, tmdK, tmdV, O, dO, LSE, dQ, dK, dV,
-                        workspace, p, num_sms, stream);
-  return launch_d<128>(tmQ, tmK, tmV, tmdO, tmL2, tmD, tmdK, tmdV, O, dO, LSE, dQ, dK, dV,
-                       workspace, p, num_sms, stream);
+    return mode == kModNone  ? launch(launch_d<64, kModNone>)
+           : mode == kModCap ? launch(launch_d<64, kModCap>)
+                             : launch(launch_d<64, kModMask>);
+  return mode == kModNone  ? launch(launch_d<128, kModNone>)
+         : mode == kModCap ? launch(launch_d<128, kModCap>)
+                           : launch(launch_d<128, kModMask>);
 }
 
 }  // namespace fa

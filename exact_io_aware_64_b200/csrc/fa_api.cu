@@ -390,6 +390,152 @@ fa_status bwd_impl(const void* Q, const void* K, const void* V, const void* O, c
   return FA_OK;
 }
 
+// ------------------------------------------------------------------ modified scores
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The modifications of a _mod call: heads, cap, slopes, prefix lengths, document ranges.
+struct ModParams {
+  int Hkv;
+  float softcap;
+  const float* slopes;
+  const int* prefix;
+  const int* doc_start;
+  const int* doc_end;
+};
+
+fa_status check_mod(const ModParams& m, int B, int H, int Nq, int Nk, int d, float scale,
+                    int causal, bool* noop) {
+  FA_TRY(check_common(B, H, Nq, Nk, d, scale, causal, noop));
+  if (m.Hkv < 0 || (H > 0 && (m.Hkv == 0 || H % m.Hkv != 0)))
+    return fail(FA_ERR_INVALID_ARG, "H=%d query heads cannot share Hkv=%d key heads", H, m.Hkv);
+  if (!(std::isfinite(m.softcap) && m.softcap >= 0.f))
+    return fail(FA_ERR_INVALID_ARG, "softcap must be finite and non-negative (0: no cap)");
+  if (m.softcap > 0.f && !(scale / m.softcap < 1e30f && m.softcap < 1e30f &&
+                           scale / m.softcap > 1e-30f))
+    return fail(FA_ERR_INVALID_ARG, "softcap %g is out of range for scale %g",
+                static_cast<double>(m.softcap), static_cast<double>(scale));
+  if (m.prefix != nullptr && !causal)
+    return fail(FA_ERR_INVALID_ARG, "prefix lengths need causal = 1");
+  if ((m.doc_start == nullptr) != (m.doc_end == nullptr))
+    return fail(FA_ERR_INVALID_ARG, "doc_start and doc_end must be given together");
+  if (!aligned4(m.slopes) || !aligned4(m.prefix) || !aligned4(m.doc_start) ||
+      !aligned4(m.doc_end))
+    return fail(FA_ERR_INVALID_ARG,
+                "slopes, prefix, doc_start and doc_end must be 4-byte aligned");
+  return FA_OK;
+}
+
+fa::Problem make_mod_problem(const ModParams& m, int B, int H, int Nq, int Nk, int d, float scale,
+                             int causal, const DeviceInfo& dev) {
+  fa::Problem p = make_problem(B, H, Nq, Nk, d, scale, causal, dev);
+  p.Hkv = m.Hkv;
+  p.softcap = m.softcap;
+  p.slopes = m.slopes;
+  p.prefix = m.prefix;
+  p.doc_start = m.doc_start;
+  p.doc_end = m.doc_end;
+  return p;
+}
+
+fa_status fwd_mod_impl(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                       const ModParams& m, int B, int H, int Nq, int Nk, int d, float scale,
+                       int causal, cudaStream_t stream) {
+  g_last_error[0] = '\0';
+  bool noop = false;
+  FA_TRY(check_mod(m, B, H, Nq, Nk, d, scale, causal, &noop));
+  if (noop) return FA_OK;
+  FA_TRY(check_ptr(Q, "Q"));
+  FA_TRY(check_ptr(K, "K"));
+  FA_TRY(check_ptr(V, "V"));
+  FA_TRY(check_ptr(O, "O"));
+  if (!aligned4(LSE)) return fail(FA_ERR_INVALID_ARG, "LSE is not 4-byte aligned");
+  const size_t qb = static_cast<size_t>(B) * H * Nq * d * 2;
+  const size_t kb = static_cast<size_t>(B) * m.Hkv * Nk * d * 2;
+  if (overlaps(O, qb, Q, qb) || overlaps(O, qb, K, kb) || overlaps(O, qb, V, kb))
+    return fail(FA_ERR_INVALID_ARG, "O overlaps an input");
+  DeviceInfo dev;
+  FA_TRY(device_info(&dev));
+  FA_TRY(require_sm100(dev));
+  CUtensorMap tmQ, tmK, tmV, tmO;
+  FA_TRY(make_tmap(&tmQ, Q, B * H, Nq, d));
+  FA_TRY(make_tmap(&tmK, K, B * m.Hkv, Nk, d));
+  FA_TRY(make_tmap(&tmV, V, B * m.Hkv, Nk, d));
+  FA_TRY(make_tmap(&tmO, O, B * H, Nq, d, 32));
+  const fa::Problem p = make_mod_problem(m, B, H, Nq, Nk, d, scale, causal, dev);
+  cudaError_t e = fa::launch_fwd_sm100(tmQ, tmK, tmV, tmO, O, LSE, p, dev.num_sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "launching the forward kernel");
+  return FA_OK;
+}
+
+fa_status bwd_mod_impl(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                       const float* LSE, void* dQ, void* dK, void* dV, const ModParams& m, int B,
+                       int H, int Nq, int Nk, int d, float scale, int causal, void* workspace,
+                       size_t workspace_bytes, cudaStream_t stream) {
+  g_last_error[0] = '\0';
+  bool noop = false;
+  FA_TRY(check_mod(m, B, H, Nq, Nk, d, scale, causal, &noop));
+  const size_t qb = static_cast<size_t>(B) * H * Nq * d * 2;
+  const size_t kb = static_cast<size_t>(B) * m.Hkv * Nk * d * 2;
+  if (noop) {
+    // keys without queries have zero gradients (see bwd_impl)
+    if (static_cast<long long>(B) * H == 0 || Nk == 0) return FA_OK;
+    FA_TRY(check_key_grads(dK, dV, kb));
+    DeviceInfo dev;
+    FA_TRY(device_info(&dev));
+    const fa::Problem p = make_problem(B, m.Hkv, Nq, Nk, d, scale, causal, dev);
+    return zero_key_grads(dK, dV, p, 2, dev, stream);
+  }
+  FA_TRY(check_ptr(Q, "Q"));
+  FA_TRY(check_ptr(K, "K"));
+  FA_TRY(check_ptr(V, "V"));
+  FA_TRY(check_ptr(O, "O"));
+  FA_TRY(check_ptr(dO, "dO"));
+  FA_TRY(check_ptr(LSE, "LSE"));
+  FA_TRY(check_ptr(dQ, "dQ"));
+  FA_TRY(check_ptr(dK, "dK"));
+  FA_TRY(check_ptr(dV, "dV"));
+  FA_TRY(check_ptr(workspace, "workspace"));
+  const size_t need = fa_bwd_workspace_bytes(B, H, Nq, d);
+  if (workspace_bytes < need)
+    return fail(FA_ERR_INVALID_ARG, "workspace has %zu bytes, %zu needed", workspace_bytes,
+                need);
+  struct Buf {
+    const void* p;
+    size_t n;
+  };
+  const size_t lb = static_cast<size_t>(B) * H * Nq * 4;
+  const Buf ins[6] = {{Q, qb}, {K, kb}, {V, kb}, {O, qb}, {dO, qb}, {LSE, lb}};
+  const Buf outs[4] = {{dQ, qb}, {dK, kb}, {dV, kb}, {workspace, need}};
+  for (int i = 0; i < 4; ++i) {
+    for (const Buf& in : ins)
+      if (overlaps(outs[i].p, outs[i].n, in.p, in.n))
+        return fail(FA_ERR_INVALID_ARG, "a gradient or the workspace overlaps an input");
+    for (int k = 0; k < i; ++k)
+      if (overlaps(outs[i].p, outs[i].n, outs[k].p, outs[k].n))
+        return fail(FA_ERR_INVALID_ARG, "gradients and workspace overlap each other");
+  }
+  DeviceInfo dev;
+  FA_TRY(device_info(&dev));
+  FA_TRY(require_sm100(dev));
+  const int BH = B * H, BHk = B * m.Hkv;
+  CUtensorMap tmQ, tmK, tmV, tmdO, tmL2, tmD, tmdK, tmdV;
+  FA_TRY(make_tmap(&tmQ, Q, BH, Nq, d));
+  FA_TRY(make_tmap(&tmK, K, BHk, Nk, d));
+  FA_TRY(make_tmap(&tmV, V, BHk, Nk, d));
+  FA_TRY(make_tmap(&tmdO, dO, BH, Nq, d));
+  FA_TRY(make_tmap(&tmdK, dK, BHk, Nk, d, 32));
+  FA_TRY(make_tmap(&tmdV, dV, BHk, Nk, d, 32));
+  const int Npad = static_cast<int>(fa::bwd_padded_rows(Nq));
+  float* ws = static_cast<float*>(workspace);
+  FA_TRY(make_row_tmap(&tmD, ws, BH, Npad));
+  FA_TRY(make_row_tmap(&tmL2, ws + static_cast<size_t>(BH) * Npad, BH, Npad));
+  const fa::Problem p = make_mod_problem(m, B, H, Nq, Nk, d, scale, causal, dev);
+  cudaError_t e = fa::launch_bwd_sm100(tmQ, tmK, tmV, tmdO, tmL2, tmD, tmdK, tmdV, O, dO, LSE,
+                                       dQ, dK, dV, ws, p, dev.num_sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "launching the backward kernels");
+  return FA_OK;
+}
+
 // The start-token arrays of the packed-layout calls: both given, 4-byte aligned.
 fa_status check_cu(const int* cu_q, const int* cu_k) {
   if (cu_q == nullptr || cu_k == nullptr)
@@ -845,6 +991,45 @@ fa_status fa_selftest_timeout(long long limit_cycles, cudaStream_t stream) {
   cudaError_t e = fa::launch_timeout_probe(limit_cycles, p, stream);
   if (e != cudaSuccess) return cuda_fail(e, "launching the timeout probe");
   return FA_OK;
+}
+
+fa_status fa_doc_ranges(const int* doc_ids, int* doc_start, int* doc_end, int B, int N,
+                        cudaStream_t stream) {
+  g_last_error[0] = '\0';
+  if (B < 0 || N < 0)
+    return fail(FA_ERR_INVALID_ARG, "sizes must be non-negative (B=%d N=%d)", B, N);
+  if (N > (1 << 30) || static_cast<long long>(B) * N >= (1ll << 31))
+    return fail(FA_ERR_INVALID_ARG, "B*N = %lld tokens is too large", static_cast<long long>(B) * N);
+  if (B == 0 || N == 0) return FA_OK;
+  if (doc_ids == nullptr || doc_start == nullptr || doc_end == nullptr)
+    return fail(FA_ERR_INVALID_ARG, "doc_ids, doc_start and doc_end are required");
+  if (!aligned4(doc_ids) || !aligned4(doc_start) || !aligned4(doc_end))
+    return fail(FA_ERR_INVALID_ARG, "doc_ids, doc_start and doc_end must be 4-byte aligned");
+  const size_t n = static_cast<size_t>(B) * N * 4;
+  if (overlaps(doc_start, n, doc_ids, n) || overlaps(doc_end, n, doc_ids, n) ||
+      overlaps(doc_start, n, doc_end, n))
+    return fail(FA_ERR_INVALID_ARG, "doc_ids, doc_start and doc_end overlap");
+  cudaError_t e = fa::launch_doc_ranges(doc_ids, doc_start, doc_end, B, N, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "launching the document-range kernel");
+  return FA_OK;
+}
+
+fa_status fa_fwd_mod(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                     const float* slopes, const int* prefix, const int* doc_start,
+                     const int* doc_end, int B, int H, int Hkv, int Nq, int Nk, int d,
+                     float scale, int causal, float softcap, cudaStream_t stream) {
+  const ModParams m{Hkv, softcap, slopes, prefix, doc_start, doc_end};
+  return fwd_mod_impl(Q, K, V, O, LSE, m, B, H, Nq, Nk, d, scale, causal, stream);
+}
+
+fa_status fa_bwd_mod(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                     const float* LSE, void* dQ, void* dK, void* dV, const float* slopes,
+                     const int* prefix, const int* doc_start, const int* doc_end, int B, int H,
+                     int Hkv, int Nq, int Nk, int d, float scale, int causal, float softcap,
+                     void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  const ModParams m{Hkv, softcap, slopes, prefix, doc_start, doc_end};
+  return bwd_mod_impl(Q, K, V, O, dO, LSE, dQ, dK, dV, m, B, H, Nq, Nk, d, scale, causal,
+                      workspace, workspace_bytes, stream);
 }
 
 fa_status fa_check_device_error(cudaStream_t stream) {

@@ -56,6 +56,7 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "mod.cuh"
 #include "sm100.cuh"
 
 namespace fa {
@@ -134,16 +135,20 @@ struct FwdArgs {
   int n_units;      // units per (batch, head) = ceil(Nq / 256)
   int total_units;  // BH * n_units
   float scale_log2;  // scale * log2(e)
+  ModArgs mod;       // modified-score calls only
 };
 
 struct UnitInfo {
   int bh, u, n0, n1;  // n_t: key tiles of query tile t (0: no work)
+  int jb, kbh;        // first key tile (modified scores: may be > 0), head of K and V
   int lq, lk, off;    // the sequence's query rows, key rows, position of query row 0
   int h, tq0, tk0;    // head; packed layout: the sequence's first query and key token
 };
 
+template <int kMode>
 __device__ __forceinline__ UnitInfo unit_info(int w, const FwdArgs& a) {
   UnitInfo r;
+  r.jb = 0;
   if (a.causal) {
     // heaviest units (largest query index) first, all heads of one row-band together
     r.u = a.n_units - 1 - w / a.BH;
@@ -157,6 +162,30 @@ __device__ __forceinline__ UnitInfo unit_info(int w, const FwdArgs& a) {
   r.h = r.bh % a.H;
   r.tq0 = 0;
   r.tk0 = 0;
+  r.kbh = r.bh;
+  if constexpr (kMode != kModNone) {
+    // both tiles walk the keys from the unit's first visible tile on; the limits rise
+    // from row to row, so a tile's first and last rows bound it
+    const int b = r.bh / a.H;
+    r.kbh = b * a.mod.Hkv + r.h / a.mod.group;
+    r.off = r.lk - r.lq;
+    int e[2];
+    r.jb = a.Nk;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int r0 = (2 * r.u + t) * kBM;
+      e[t] = 0;
+      if (r0 >= r.lq) continue;
+      const int lo = mod_row(a.mod, b, r0, r.off, a.Nk, a.causal).lo;
+      const int hi = mod_row(a.mod, b, min(r0 + kBM, r.lq) - 1, r.off, a.Nk, a.causal).hi;
+      if (hi <= lo) continue;  // no row of the tile sees a key
+      r.jb = min(r.jb, lo / kBN);
+      e[t] = (hi + kBN - 1) / kBN;
+    }
+    r.n0 = max(e[0] - r.jb, 0);
+    r.n1 = max(e[1] - r.jb, 0);
+    return r;
+  }
   if (a.cu_q != nullptr) {
     const int b = r.bh / a.H;
     r.tq0 = a.cu_q[b];
@@ -191,7 +220,7 @@ __device__ __forceinline__ UnitInfo unit_info(int w, const FwdArgs& a) {
   return r;
 }
 
-template <int D>
+template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
@@ -220,6 +249,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool packed = args.cu_q != nullptr;
   auto tma_y = [&](const UnitInfo& ui, int row) { return packed ? ui.h : row; };
   auto tma_z = [&](const UnitInfo& ui, int t0, int row) { return packed ? t0 + row : ui.bh; };
+  auto tma_zk = [&](const UnitInfo& ui, int row) {
+    if constexpr (kMode != kModNone) return ui.kbh;
+    return tma_z(ui, ui.tk0, row);
+  };
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -275,10 +308,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t issued_phase[L::kStages];
       for (int s = 0; s < L::kStages; ++s) issued[s] = 0, issued_phase[s] = 0;
       for (int r = 0, w = snake_unit(0); ok && w < args.total_units; w = snake_unit(++r)) {
-        const UnitInfo ui = unit_info(w, args);
-        if (ui.n0 == 0) continue;  // no query rows in this unit (every role skips it)
+        const UnitInfo ui = unit_info<kMode>(w, args);
+        if (ui.n0 == 0 && ui.n1 == 0) continue;  // no work in this unit (every role skips it)
         for (int t = 0; t < 2 && ok; ++t) {
-          if (t == 1 && ui.n1 == 0) break;
+          if ((t == 0 ? ui.n0 : ui.n1) == 0) continue;
           if (q_uses[t] > 0)
             ok = wait_warp(bar(L::kBarQEmpty + t), (q_uses[t] - 1) & 1);
           if (!ok) break;
@@ -300,8 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t dst = base + L::kRing + stage * L::kTileBytes;
             const CUtensorMap* tm = kv == 0 ? &tmK : &tmV;
             for (int c = 0; c < D / 64; ++c)
-              tma_load_3d_elect(dst + c * L::kBoxBytes, tm, fb, c * 64, tma_y(ui, j * kBN),
-                                tma_z(ui, ui.tk0, j * kBN));
+              tma_load_3d_elect(dst + c * L::kBoxBytes, tm, fb, c * 64,
+                                tma_y(ui, (ui.jb + j) * kBN), tma_zk(ui, (ui.jb + j) * kBN));
             issued[stage] = 1;
             issued_phase[stage] = phase;
             if (++stage == L::kStages) stage = 0, phase ^= 1;
@@ -378,8 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ring = 0;
         int s_tot[2] = {0, 0};
         for (int r = 0, w = snake_unit(0); ok && w < args.total_units; w = snake_unit(++r)) {
-          const UnitInfo ui = unit_info(w, args);
-          if (ui.n0 == 0) continue;  // no query rows in this unit
+          const UnitInfo ui = unit_info<kMode>(w, args);
+          if (ui.n0 == 0 && ui.n1 == 0) continue;  // no work in this unit
           const int nt[2] = {ui.n0, ui.n1};
           const int n = max(ui.n0, ui.n1);
           for (int t = 0; t < 2 && ok; ++t)
@@ -452,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
       for (int r = 0, w = snake_unit(0); ok && w < args.total_units; w = snake_unit(++r)) {
-        const UnitInfo ui = unit_info(w, args);
-        if (ui.n0 == 0) continue;  // no query rows in this unit
+        const UnitInfo ui = unit_info<kMode>(w, args);
+        if (ui.n0 == 0 && ui.n1 == 0) continue;  // no work in this unit
         const int nt[2] = {ui.n0, ui.n1};
         const int n = max(ui.n0, ui.n1);
         for (int t = 0; t < 2 && ok; ++t)
@@ -517,11 +550,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool st_used = false;  // this warp's O staging box has been handed to a bulk store
     bool ok = true;
     for (int r = 0, w = snake_unit(0); ok && w < args.total_units; w = snake_unit(++r)) {
-      const UnitInfo ui = unit_info(w, args);
+      const UnitInfo ui = unit_info<kMode>(w, args);
       const int n_t = t == 0 ? ui.n0 : ui.n1;
-      if (n_t == 0) continue;
       const int qt = 2 * ui.u + t;
       const int q_row = qt * kBM + row;
+      if (n_t == 0) {
+        if constexpr (kMode != kModNone) {
+          // rows that see no key: O = 0, LSE = -inf
+          if (q_row < ui.lq) {
+            const size_t at = static_cast<size_t>(ui.bh) * args.Nq + q_row;
+            uint4* o = reinterpret_cast<uint4*>(args.O + at * D);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (args.LSE != nullptr) args.LSE[at] = -INFINITY;
+          }
+        }
+        continue;
+      }
+      // modified scores: this row's visible keys, the keys that every row of the tile
+      // sees, the tile's positions and the head's slope (log2 units)
+      RowLimits lim_row{0, 0};
+      int full_lo = 0, full_hi = 0, pos0 = 0, pos1 = 0;
+      float slope2 = 0.f;
+      if constexpr (kMode != kModNone) {
+        const int b = ui.bh / args.H;
+        const int first = qt * kBM, last = min(first + kBM, ui.lq) - 1;
+        lim_row = mod_row(args.mod, b, min(q_row, last), ui.off, args.Nk, args.causal);
+        full_lo = mod_row(args.mod, b, last, ui.off, args.Nk, args.causal).lo;
+        full_hi = mod_row(args.mod, b, first, ui.off, args.Nk, args.causal).hi;
+        pos0 = first + ui.off;
+        pos1 = first + kBM - 1 + ui.off;
+        if (args.mod.slopes != nullptr) slope2 = args.mod.slopes[ui.h] * kLog2e;
+      }
       float m = -INFINITY;  // running max, log2 units (scaled logits * log2 e)
       float l = 0.f;
       for (int j = 0; j < n_t; ++j) {
@@ -538,11 +598,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         float s[kBN];
 #pragma unroll
         for (int c = 0; c < kBN; ++c) s[c] = __uint_as_float(sr[c]);
-        const int kv0 = j * kBN;
+        const int kv0 = (ui.jb + j) * kBN;
+        // log2-unit score of entry c: s[c] * unit + shift
+        float unit = args.scale_log2, shift = 0.f;
+        if constexpr (kMode != kModNone) {
+          if constexpr (kMode == kModCap) {
+            tanh_scores<kBN>(s, args.mod);
+            unit = args.mod.cap_log2;
+          }
+          if (slope2 != 0.f) {
+            // -slope |p - j|, p the row's position: linear in the key inside a tile that
+            // lies wholly before or after the query tile, and the row's constant part is
+            // then added after the maximum
+            const float p = static_cast<float>(q_row + ui.off);
+            if (kv0 + kBN - 1 <= pos0 || kv0 >= pos1) {
+              const float sl = kv0 >= pos1 ? -slope2 : slope2;
+              shift = sl * (static_cast<float>(kv0) - p);
+              const uint64_t u2 = f32x2(unit, unit), step = f32x2(2.f * sl, 2.f * sl);
+              uint64_t b2 = f32x2(0.f, sl);
+#pragma unroll
+              for (int c = 0; c < kBN; c += 2) {
+                f32x2_split(fma_x2(f32x2(s[c], s[c + 1]), u2, b2), s[c], s[c + 1]);
+                b2 = add_x2(b2, step);
+              }
+            } else {
+              const float d0 = static_cast<float>(kv0) - p;
+#pragma unroll
+              for (int c = 0; c < kBN; ++c)
+                s[c] = s[c] * unit - slope2 * fabsf(d0 + static_cast<float>(c));
+            }
+            unit = 1.f;
+          }
+          if (kv0 < full_lo || kv0 + kBN > full_hi) {
+            const int lo = lim_row.lo - kv0;
+            const unsigned width = static_cast<unsigned>(lim_row.hi - lim_row.lo);
+#pragma unroll
+            for (int c = 0; c < kBN; ++c)
+              if (static_cast<unsigned>(c - lo) >= width) s[c] = -INFINITY;
+          }
+        }
         // a ragged last key tile, or (causal) a tile whose last key lies past the
         // position of the tile's first row
-        const bool need_mask = (kv0 + kBN > ui.lk) ||
-                               (args.causal && kv0 + kBN - 1 > qt * kBM + ui.off);
+        const bool need_mask = kMode == kModNone &&
+                               ((kv0 + kBN > ui.lk) ||
+                                (args.causal && kv0 + kBN - 1 > qt * kBM + ui.off));
         if (need_mask) {
           const int lim = args.causal ? min(ui.lk, q_row + ui.off + 1) : ui.lk;
 #pragma unroll
@@ -558,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 8; c < kBN; c += 2) mx8[(c / 2) % 8] = max3(mx8[(c / 2) % 8], s[c], s[c + 1]);
         const float mx = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]),
                               fmaxf(mx8[6], mx8[7]));
-        const float m_tile = mx * args.scale_log2;
+        const float m_tile = kMode == kModNone ? mx * args.scale_log2 : fmaf(mx, unit, shift);
         float alpha = 1.f;
         bool rescale = false;
         if (m_tile > m + kRescaleThreshold || m == -INFINITY) {
@@ -593,8 +692,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // p = 2^(s * scale * log2e - m): the scale-and-subtract and the row sum run on
         // packed float pairs (one instruction per two entries), the exponentials on MUFU
         uint32_t pk[kBN / 2];
-        const uint64_t scale2 = f32x2(args.scale_log2, args.scale_log2);
-        const uint64_t negm2 = f32x2(-mref, -mref);
+        const float sc = kMode == kModNone ? args.scale_log2 : unit;
+        const float negm = kMode == kModNone ? -mref : shift - mref;
+        const uint64_t scale2 = f32x2(sc, sc);
+        const uint64_t negm2 = f32x2(negm, negm);
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int c = 0; c < kBN / 2; ++c) {
@@ -630,7 +731,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       o_count += n_t;
       tc_fence_after();
-      const float inv_l = 1.f / l;
+      // (a row that sees none of the unit's keys has l = 0: O = 0, LSE = -inf)
+      const float inv_l = kMode != kModNone && l == 0.f ? 0.f : 1.f / l;
       const int bh = ui.bh;
       __nv_bfloat16* orow =
           args.O + (packed ? (static_cast<size_t>(ui.tq0 + q_row) * args.H + ui.h) * D
@@ -694,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (args.LSE != nullptr && q_row < ui.lq)
         args.LSE[packed ? static_cast<size_t>(ui.h) * args.total_q + ui.tq0 + q_row
                         : static_cast<size_t>(bh) * args.Nq + q_row] =
-            (m + __log2f(l)) * 0.69314718055994531f;
+            kMode != kModNone && l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
     }
     // the bulk stores this thread issued have completed before the CTA (and its shared
     // memory) goes away
@@ -710,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, int kMode>
 cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                      const CUtensorMap& tmO, void* O, float* LSE, const Problem& p, int num_sms,
                      cudaStream_t stream) {
@@ -732,19 +834,20 @@ cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   a.causal = p.causal;
   a.n_units = (p.N + 2 * kBM - 1) / (2 * kBM);
   a.total_units = p.BH * a.n_units;
-  a.scale_log2 = p.scale * 1.4426950408889634f;
+  a.scale_log2 = p.scale * kLog2e;
+  a.mod = mod_args(p);
   // The register split inside the kernel assumes exactly kRegsLaunch registers a thread
   // at launch; with fewer, the softmax warpgroups' increase could never be granted.
   cudaFuncAttributes fattr;
-  cudaError_t e = cudaFuncGetAttributes(&fattr, fwd_sm100_kernel<D>);
+  cudaError_t e = cudaFuncGetAttributes(&fattr, fwd_sm100_kernel<D, kMode>);
   if (e != cudaSuccess) return e;
   if (fattr.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(fwd_sm100_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           L::kAlloc);
+  e = cudaFuncSetAttribute(fwd_sm100_kernel<D, kMode>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return e;
   const int grid = a.total_units < num_sms ? a.total_units : num_sms;
   if ((e = trace_mark(p, 0, stream)) != cudaSuccess) return e;
-  fwd_sm100_kernel<D><<<grid, kThreads, L::kAlloc, stream>>>(tmQ, tmK, tmV, tmO, a);
+  fwd_sm100_kernel<D, kMode><<<grid, kThreads, L::kAlloc, stream>>>(tmQ, tmK, tmV, tmO, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return trace_mark(p, 1, stream);
 }
@@ -754,8 +857,15 @@ cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
 cudaError_t launch_fwd_sm100(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                              const CUtensorMap& tmV, const CUtensorMap& tmO, void* O, float* LSE,
                              const Problem& p, int num_sms, cudaStream_t stream) {
-  if (p.d == 64) return launch_d<64>(tmQ, tmK, tmV, tmO, O, LSE, p, num_sms, stream);
-  return launch_d<128>(tmQ, tmK, tmV, tmO, O, LSE, p, num_sms, stream);
+  auto launch = [&](auto* kernel) { return kernel(tmQ, tmK, tmV, tmO, O, LSE, p, num_sms, stream); };
+  const int mode = mod_mode(p);
+  if (p.d == 64)
+    return mode == kModNone  ? launch(launch_d<64, kModNone>)
+           : mode == kModCap ? launch(launch_d<64, kModCap>)
+                             : launch(launch_d<64, kModMask>);
+  return mode == kModNone  ? launch(launch_d<128, kModNone>)
+         : mode == kModCap ? launch(launch_d<128, kModCap>)
+                           : launch(launch_d<128, kModMask>);
 }
 
 }  // namespace fa

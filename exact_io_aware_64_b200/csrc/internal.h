@@ -35,6 +35,14 @@ struct Problem {
   // trace[k] after the k-th; n_trace entries
   cudaEvent_t* trace;
   int n_trace;
+  // modified-score calls (mod.cuh; all zero otherwise): Hkv key heads per sequence, each
+  // shared by H / Hkv query heads, so K and V (dK, dV) are [B*Hkv, Nk, d]
+  int Hkv;
+  float softcap;         // 0: none
+  const float* slopes;   // [H] or null
+  const int* prefix;     // [B] or null
+  const int* doc_start;  // [B][Nk] or null (both)
+  const int* doc_end;
 };
 
 // Record trace event k of `p` on `stream` if the caller asked for it.
@@ -91,6 +99,10 @@ cudaError_t launch_merge(float* O_acc, float* LSE_acc, const void* O_part,
 // bf16(acc[i]) when out is not null.
 cudaError_t launch_accumulate(float* acc, const void* part, void* out, long long n,
                               const Problem& p, cudaStream_t stream);
+
+// Runs of equal document ids ([B][N]): first token, and one past the last, of each token's.
+cudaError_t launch_doc_ranges(const int* ids, int* start, int* end, int B, int N,
+                              cudaStream_t stream);
 
 // One warp waiting on an mbarrier nothing arrives on, giving up after limit_cycles with
 // the kernels' timeout error (a check of the failure path).

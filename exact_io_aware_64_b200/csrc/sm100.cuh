@@ -418,6 +418,12 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Packed float32 pairs (sm_100 executes fma/add/mul on two floats per instruction).
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
   uint64_t r;

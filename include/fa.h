@@ -297,6 +297,65 @@ FA_API fa_status fa_bwd_f32_packed(const float* Q, const float* K, const float* 
                                    size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Document ranges: from a document id per token to the run of equal ids each token lies
+ * in, as the _mod calls take documents (no counterpart on the pages).
+ *   doc_ids            in : [B,N] int32; a negative id marks a padding token
+ *   doc_start, doc_end out: [B,N] int32: the run's first token and one past its last
+ *                      (both j for a padding token j, which is then in no document)
+ * Equal ids that are not neighbours are different documents.  One call serves every
+ * layer's forward and backward calls over the same batch.  Pointers 4-byte aligned and
+ * not overlapping; B*N < 2^31, N <= 2^30; one kernel on `stream`.
+ */
+FA_API fa_status fa_doc_ranges(const int* doc_ids, int* doc_start, int* doc_end, int B, int N,
+                               cudaStream_t stream);
+
+/*
+ * Forward pass with modified scores and shared key heads, bf16 (no counterpart on the
+ * pages).  With p_i = i + Nk - Nq the position of query row i (as in fa_fwd_qk) and h'
+ * = h / (H / Hkv) the key head of query head h:
+ *   z = scale q_i . k_j;   x = softcap tanh(z / softcap) if softcap > 0, else z;
+ *   x -= slopes[h] |p_i - j| if slopes is given;
+ *   j is visible to i when (not causal, or j <= p_i, or j < prefix[b]) and, if document
+ *   ranges are given, p_i and j lie in the same document (a row with p_i < 0 in none);
+ *   O = softmax over the visible keys of x times V, LSE = log sum exp x.
+ *   Q   in : [B,H,Nq,d] bf16;  K, V in : [B,Hkv,Nk,d] bf16, H a multiple of Hkv
+ *   O   out: [B,H,Nq,d] bf16, must not overlap Q, K or V;  LSE out: [B,H,Nq] float32 or NULL
+ *   slopes  in : [H] float32 or NULL (finite; they are constants, no gradient is formed)
+ *   prefix  in : [B] int32 or NULL: keys below it are visible to every row of sequence b
+ *                (of the same document); needs causal = 1; taken as min(prefix, Nk), and
+ *                a negative one as 0
+ *   doc_start, doc_end in : [B,Nk] int32 from fa_doc_ranges over the key tokens, or both NULL
+ *   softcap >= 0 and finite; 0 is no cap; d, scale, causal as in fa_fwd_qk.
+ * A row that sees no key gets O = 0 and LSE = -inf.  K and V must hold finite values in
+ * every row, visible or not (a hidden key's probability is zero, and 0 times a NaN is a
+ * NaN).  doc_start and doc_end arrays of other origin that do not rise along the sequence
+ * give unspecified results.  One kernel; errors and asynchrony as fa_fwd.
+ */
+FA_API fa_status fa_fwd_mod(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                            const float* slopes, const int* prefix, const int* doc_start,
+                            const int* doc_end, int B, int H, int Hkv, int Nq, int Nk, int d,
+                            float scale, int causal, float softcap, cudaStream_t stream);
+
+/*
+ * Backward pass of fa_fwd_mod with the same modifications: P = exp(x - LSE), dV = P^T dO,
+ * dP = dO V^T, D = rowsum(dO * O), dS = P (dP - D) (1 - tanh^2(z / softcap)) (the last
+ * factor with a cap), dQ = scale dS K, dK = scale dS^T Q; dK and dV are summed over the
+ * query heads that share a key head, in float32, in a fixed order.
+ *   Q, O, dO in : [B,H,Nq,d] bf16;  K, V in : [B,Hkv,Nk,d] bf16;  LSE in : [B,H,Nq] float32
+ *   dQ out: [B,H,Nq,d] bf16;  dK, dV out: [B,Hkv,Nk,d] bf16
+ *   workspace: fa_bwd_workspace_bytes(B,H,Nq,d) bytes, 16-byte aligned
+ * Every row of dQ, dK and dV is written: zeros for a row that sees no key and for a key
+ * that no row sees (also when Nq == 0).  Gradients and workspace must not overlap each
+ * other or an input.  Three kernels, no atomics; otherwise as fa_bwd_qk.
+ */
+FA_API fa_status fa_bwd_mod(const void* Q, const void* K, const void* V, const void* O,
+                            const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
+                            const float* slopes, const int* prefix, const int* doc_start,
+                            const int* doc_end, int B, int H, int Hkv, int Nq, int Nk, int d,
+                            float scale, int causal, float softcap, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Merge a partial attention result into an accumulator ("FlashAttention, simplified",
  * "The trick": the rescale-and-add step of the online softmax, applied to two results
  * over disjoint key sets, as context-parallel attention needs when each GPU holds a
