@@ -29,6 +29,7 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 SIGNATURES = {
     "fa_abi_version": ([], _i),
@@ -64,6 +65,10 @@ SIGNATURES = {
     "fa_doc_ranges": ([_vp, _vp, _vp, _i, _i, _vp], _i),
     "fa_fwd_mod": ([_vp] * 9 + [_i] * 6 + [_f, _i, _f, _vp], _i),
     "fa_bwd_mod": ([_vp] * 13 + [_i] * 6 + [_f, _i, _f, _vp, _sz, _vp], _i),
+    "fa_rotary": ([_vp] * 6 + [_ll] + [_i] * 8 + [_f, _vp, _vp, _vp], _i),
+    "fa_rotary_f32": ([_vp] * 6 + [_ll] + [_i] * 8 + [_f, _vp, _vp, _vp], _i),
+    "fa_fwd_tree_workspace_bytes": ([_i] * 5, _sz),
+    "fa_fwd_tree": ([_vp] * 9 + [_i] * 8 + [_f, _f, _vp, _sz, _vp], _i),
     "fa_merge": ([_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp], _i),
     "fa_accumulate": ([_vp, _vp, _vp, _sz, _vp], _i),
     "fa_selftest_timeout": ([ctypes.c_longlong, _vp], _i),
@@ -564,6 +569,174 @@ def bwd_mod(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tensor,
                               _stream_handle(stream))
     _check("fa_bwd_mod", st)
     return dQ, dK, dV
+
+
+def rotary_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0,
+                       scaling: str = "linear", original_len: int = 8192,
+                       device="cuda"):
+    """Inverse frequencies [rot/2] float32 and the scale for ``rotary``: base^(-2k/rot),
+    stretched ``factor`` times for contexts longer than the ``original_len`` tokens a model
+    was trained on.
+
+    "linear": every frequency divided by factor.  "base": the base raised to base *
+    factor^(rot / (rot - 2)), which divides the slowest frequency by factor and leaves the
+    fastest.  "parts": frequencies that turn at least 32 times within original_len are
+    kept, those that turn less than once are divided by factor, those between are blended
+    linearly in the number of turns' place between the two limits (in log space), and the
+    scale is 0.1 ln(factor) + 1.  Returns (inv_freq, mscale)."""
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even and positive")
+    if not factor > 0 or not base > 0:
+        raise ValueError("base and factor must be positive")
+    k = torch.arange(rot // 2, dtype=torch.float64)
+    mscale = 1.0
+    if scaling == "linear":
+        freq = base ** (-2 * k / rot) / factor
+    elif scaling == "base":
+        if rot > 2:
+            base = base * factor ** (rot / (rot - 2))
+        freq = base ** (-2 * k / rot)
+    elif scaling == "parts":
+        freq = base ** (-2 * k / rot)
+        turns = original_len * freq / (2 * math.pi)
+        keep = (torch.log(turns) / math.log(32.0)).clamp(0, 1)
+        freq = freq * (keep + (1 - keep) / factor)
+        mscale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    else:
+        raise ValueError("scaling must be 'linear', 'base' or 'parts'")
+    return freq.float().to(device), mscale
+
+
+def _rotary_side(name, x, out, dtype, device):
+    """(B, heads, N, d) and the stride array of one tensor of a rotary call."""
+    for what, t in ((name, x), (f"{name}'s output", out)):
+        if not t.is_cuda or t.device != device:
+            raise ValueError(f"{what} must be on the inputs' CUDA device")
+        if t.dtype != dtype:
+            raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+        if t.dim() not in (3, 4) or t.shape != x.shape:
+            raise ValueError(f"{what} must be [B, heads, N, d] or packed [tokens, heads, d]")
+        if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{what} must be contiguous in its last dimension")
+    if x.dim() == 3:
+        N, heads, d = x.shape
+        st = [0, x.stride(1), x.stride(0), 0, out.stride(1), out.stride(0)]
+        return (1, heads, N, d), (_ll * 6)(*st)
+    return tuple(x.shape), (_ll * 6)(*x.stride()[:3], *out.stride()[:3])
+
+
+def _rotary(Q, K, inv_freq, positions, first, interleaved, mscale, Q_out, K_out, inverse, stream):
+    dtype, device = Q.dtype, Q.device
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("Q and K must be bfloat16 or float32")
+    Q_out = torch.empty_like(Q) if Q_out is None else Q_out
+    (B, H, N, d), qs = _rotary_side("Q", Q, Q_out, dtype, device)
+    Hkv, ks = 0, None
+    if K is not None:
+        K_out = torch.empty_like(K) if K_out is None else K_out
+        (Bk, Hkv, Nk, dk), ks = _rotary_side("K", K, K_out, dtype, device)
+        if (Bk, Nk, dk) != (B, N, d) or K.dim() != Q.dim():
+            raise ValueError("Q and K must agree in batch, tokens and head dimension")
+    elif K_out is not None:
+        raise ValueError("K_out without K")
+    R = 2 * inv_freq.numel()
+    _check_vec("inv_freq", inv_freq, (R // 2,), torch.float32, device)
+    if positions is not None:
+        shape = (N,) if Q.dim() == 3 else (B, N)
+        _check_vec("positions", positions, shape, torch.int32, device)
+    name = "fa_rotary" if dtype == torch.bfloat16 else "fa_rotary_f32"
+    with torch.cuda.device(device):
+        st = getattr(lib(), name)(_ptr(Q), _ptr(Q_out), _ptr(K), _ptr(K_out), _ptr(inv_freq),
+                                  _ptr(positions), int(first), B, H, Hkv, N, d, R,
+                                  int(bool(interleaved)), int(inverse), float(mscale), qs, ks,
+                                  _stream_handle(stream))
+    _check(name, st)
+    return Q_out, K_out
+
+
+def rotary(Q: torch.Tensor, K: Optional[torch.Tensor], inv_freq: torch.Tensor,
+           positions: Optional[torch.Tensor] = None, first: int = 0, interleaved: bool = False,
+           mscale: float = 1.0, Q_out: Optional[torch.Tensor] = None,
+           K_out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Rotary positions of Q [B, H, N, d] and K [B, Hkv, N, d] (or None) in one launch
+    through ``fa_rotary`` (bf16) or ``fa_rotary_f32``; packed [tokens, heads, d] tensors
+    too.  The first 2 * len(inv_freq) elements of each head are turned in pairs (k, k + R/2),
+    or (2k, 2k + 1) when ``interleaved``, by position * inv_freq[k]; positions [B, N] (packed:
+    [tokens]) int32, or ``first`` + the token's number.  Any strides with contiguous rows;
+    ``Q_out=Q, K_out=K`` works in place.  Returns (Q_out, K_out)."""
+    return _rotary(Q, K, inv_freq, positions, first, interleaved, mscale, Q_out, K_out, 0, stream)
+
+
+def rotary_bwd(dQ_out: torch.Tensor, dK_out: Optional[torch.Tensor], inv_freq: torch.Tensor,
+               positions: Optional[torch.Tensor] = None, first: int = 0,
+               interleaved: bool = False, mscale: float = 1.0,
+               dQ: Optional[torch.Tensor] = None, dK: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None):
+    """The gradient of ``rotary``: gradients of its outputs to gradients of its inputs (the
+    same map with the angles' signs turned).  Returns (dQ, dK)."""
+    return _rotary(dQ_out, dK_out, inv_freq, positions, first, interleaved, mscale, dQ, dK, 1,
+                   stream)
+
+
+def tree_workspace_bytes(B: int, H: int, Hkv: int, T: int, d: int) -> int:
+    return int(lib().fa_fwd_tree_workspace_bytes(B, H, Hkv, T, d))
+
+
+def fwd_tree(Q: torch.Tensor, K_cache: torch.Tensor, V_cache: torch.Tensor,
+             block_table: torch.Tensor, cache_lens: torch.Tensor,
+             seqlens_q: Optional[torch.Tensor] = None, tree_mask: Optional[torch.Tensor] = None,
+             scale: Optional[float] = None, softcap: float = 0.0,
+             O: Optional[torch.Tensor] = None, LSE: Optional[torch.Tensor] = None,
+             want_lse: bool = True, workspace: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None):
+    """Attention of T drafted tokens per sequence (T = 1: single-token decoding) over a paged
+    cache through ``fa_fwd_tree`` (bf16).
+
+    Q [B, H, T, d]; K_cache, V_cache [num_pages, Hkv, page, d]; block_table [B, max_pages]
+    int32; cache_lens [B] int32, drafted tokens included (they are the cache's last);
+    seqlens_q [B] int32: drafted tokens of each sequence (default T); tree_mask [B, T]
+    int64: bit u of row t lets drafted token t see drafted token u (default: a chain).
+    Rows behind a sequence's drafted tokens are not written (outputs allocated here start
+    as zeros and -inf when ``seqlens_q`` is given).  Returns (O, LSE); LSE is None when
+    ``want_lse`` is False and none is passed."""
+    if Q.dim() != 4 or K_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("Q must be [B, H, T, d], the caches [num_pages, Hkv, page, d] and "
+                         "block_table [B, max_pages]")
+    B, H, T, d = Q.shape
+    num_pages, Hkv, page, _ = K_cache.shape
+    max_pages = block_table.shape[1]
+    _check_bhnd("Q", Q, (B, H, T, d), torch.bfloat16)
+    for name, t in (("K_cache", K_cache), ("V_cache", V_cache)):
+        _check_bhnd(name, t, (num_pages, Hkv, page, d), torch.bfloat16)
+    _check_device(Q.device, K_cache=K_cache, V_cache=V_cache)
+    _check_vec("block_table", block_table, (B, max_pages), torch.int32, Q.device)
+    _check_vec("cache_lens", cache_lens, (B,), torch.int32, Q.device)
+    _check_vec("seqlens_q", seqlens_q, (B,), torch.int32, Q.device)
+    _check_vec("tree_mask", tree_mask, (B, T), torch.int64, Q.device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if O is None:
+        O = torch.empty_like(Q) if seqlens_q is None else torch.zeros_like(Q)
+    _check_bhnd("O", O, (B, H, T, d), torch.bfloat16)
+    if LSE is None and want_lse:
+        LSE = torch.full((B, H, T), float("-inf"), device=Q.device) if seqlens_q is not None \
+            else torch.empty((B, H, T), device=Q.device, dtype=torch.float32)
+    _check_vec("LSE", LSE, (B, H, T), torch.float32, Q.device)
+    if workspace is None:
+        workspace = torch.empty(max(tree_workspace_bytes(B, H, Hkv, T, d), 16), device=Q.device,
+                                dtype=torch.uint8)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _check_device(Q.device, O=O, workspace=workspace)
+    ws_bytes = workspace.numel() * workspace.element_size()
+    with torch.cuda.device(Q.device):
+        st = lib().fa_fwd_tree(_ptr(Q), _ptr(K_cache), _ptr(V_cache), _ptr(O), _ptr(LSE),
+                               _ptr(block_table), _ptr(cache_lens), _ptr(seqlens_q),
+                               _ptr(tree_mask), B, H, Hkv, T, num_pages, page, max_pages, d,
+                               float(scale), float(softcap), _ptr(workspace), ws_bytes,
+                               _stream_handle(stream))
+    _check("fa_fwd_tree", st)
+    return O, LSE
 
 
 def merge(O_acc: torch.Tensor, LSE_acc: torch.Tensor, O_part: torch.Tensor,

@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libfa.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["fa_api.cu", "fwd_sm100.cu", "fwd_f32.cu", "bwd_sm100.cu", "bwd_f32.cu", "merge.cu", "selftest.cu",
-           "zero_rows.cu", "doc_ranges.cu"]
+           "zero_rows.cu", "doc_ranges.cu", "rotary.cu", "tree_sm100.cu"]
 HEADERS = ["sm100.cuh", "internal.h", "f32_seq.cuh", "mod.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

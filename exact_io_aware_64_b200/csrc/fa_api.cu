@@ -536,6 +536,221 @@ fa_status bwd_mod_impl(const void* Q, const void* K, const void* V, const void* 
   return FA_OK;
 }
 
+// ------------------------------------------------------------------ rotary positions
+// One tensor of heads of a rotary call.  strides: {in b, h, n, out b, h, n} in elements, or
+// null for contiguous [B,heads,N,d] on both sides.
+fa_status rotary_tensor(const char* name, const void* in, void* out, int heads, int B, int N,
+                        int d, const long long* strides, int elem, fa::RotaryTensor* x) {
+  *x = fa::RotaryTensor{};
+  if (heads < 0) return fail(FA_ERR_INVALID_ARG, "%s has %d heads", name, heads);
+  if (heads == 0) return FA_OK;
+  if (static_cast<long long>(heads) * N > 0x7fffffffll / B)
+    return fail(FA_ERR_INVALID_ARG, "%s: heads * tokens is too large", name);
+  if (in == nullptr || out == nullptr)
+    return fail(FA_ERR_INVALID_ARG, "%s or its output is NULL", name);
+  if ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) % elem)
+    return fail(FA_ERR_INVALID_ARG, "%s or its output is not aligned to its elements", name);
+  const long long dense_n = d, dense_h = dense_n * N, dense_b = dense_h * heads;
+  const long long dense[6] = {dense_b, dense_h, dense_n, dense_b, dense_h, dense_n};
+  const long long* s = strides != nullptr ? strides : dense;
+  size_t extent[2];
+  for (int o = 0; o < 2; ++o) {
+    const long long n[3] = {B, heads, N};
+    long long last = d;
+    for (int k = 0; k < 3; ++k) {
+      const long long st = s[3 * o + k];
+      if (st < 0 || st > (1ll << 40))
+        return fail(FA_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40]", name);
+      if (n[k] > 1 && st > ((1ll << 46) - last) / (n[k] - 1))
+        return fail(FA_ERR_INVALID_ARG, "%s spans too many elements", name);
+      // rows of the output must not share elements
+      if (o == 1 && n[k] > 1 && st < d)
+        return fail(FA_ERR_INVALID_ARG, "%s: an output stride is below d", name);
+      last += (n[k] - 1) * st;
+    }
+    extent[o] = static_cast<size_t>(last) * elem;
+  }
+  const bool in_place = in == out && s[0] == s[3] && s[1] == s[4] && s[2] == s[5];
+  if (!in_place && overlaps(in, extent[0], out, extent[1]))
+    return fail(FA_ERR_INVALID_ARG, "%s overlaps its output and is not the same tensor", name);
+  *x = fa::RotaryTensor{in, out, heads, s[0], s[1], s[2], s[3], s[4], s[5]};
+  return FA_OK;
+}
+
+fa_status rotary_impl(const void* Q, void* Q_out, const void* K, void* K_out,
+                      const float* inv_freq, const int* positions, long long first, int B, int H,
+                      int Hkv, int N, int d, int R, int interleaved, int inverse, float mscale,
+                      const long long* q_strides, const long long* k_strides, int elem,
+                      cudaStream_t stream) {
+  g_last_error[0] = '\0';
+  if (B < 0 || N < 0)
+    return fail(FA_ERR_INVALID_ARG, "sizes must be non-negative (B=%d N=%d)", B, N);
+  if (d < 2 || d > 512) return fail(FA_ERR_UNSUPPORTED, "head dimension d=%d (2 to 512)", d);
+  if (R < 0 || R > d || R % 2)
+    return fail(FA_ERR_INVALID_ARG, "R=%d must be even and at most d=%d", R, d);
+  if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1))
+    return fail(FA_ERR_INVALID_ARG, "interleaved and inverse must be 0 or 1");
+  if (!std::isfinite(mscale)) return fail(FA_ERR_INVALID_ARG, "mscale must be finite");
+  if (first < -(1ll << 40) || first > (1ll << 40))
+    return fail(FA_ERR_INVALID_ARG, "first must be within +-2^40");
+  if (static_cast<long long>(B) * N >= (1ll << 31))
+    return fail(FA_ERR_INVALID_ARG, "B*N = %lld tokens is too large",
+                static_cast<long long>(B) * N);
+  if (B == 0 || N == 0) return FA_OK;
+  fa::RotaryArgs a{};
+  FA_TRY(rotary_tensor("Q", Q, Q_out, H, B, N, d, q_strides, elem, &a.x[0]));
+  FA_TRY(rotary_tensor("K", K, K_out, Hkv, B, N, d, k_strides, elem, &a.x[1]));
+  if (H == 0 && Hkv == 0) return FA_OK;
+  if (H > 0 && Hkv > 0 && Q_out == K_out)
+    return fail(FA_ERR_INVALID_ARG, "Q and K have the same output");
+  if (R > 0 && inv_freq == nullptr) return fail(FA_ERR_INVALID_ARG, "inv_freq is NULL");
+  if (!aligned4(inv_freq) || !aligned4(positions))
+    return fail(FA_ERR_INVALID_ARG, "inv_freq and positions must be 4-byte aligned");
+  a.inv_freq = inv_freq;
+  a.positions = positions;
+  a.first = first;
+  a.total = static_cast<long long>(B) * N;
+  a.N = N;
+  a.d = d;
+  a.R = R;
+  a.interleaved = interleaved;
+  a.copy_rest = (H > 0 && Q != Q_out) || (Hkv > 0 && K != K_out);
+  a.mscale = mscale;
+  a.sign = inverse ? -1.f : 1.f;
+  if (R == 0 && !a.copy_rest) return FA_OK;
+  DeviceInfo dev;
+  FA_TRY(device_info(&dev));
+  cudaError_t e = fa::launch_rotary(a, elem, dev.num_sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "launching the rotary kernel");
+  return FA_OK;
+}
+
+// ------------------------------------------------------------------ paged cache
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Rows of a key head, its pairs of row tiles, workspace rows of a piece and pieces.
+struct TreeSplit {
+  long long rows, pairs, piece_rows, pieces;
+};
+
+TreeSplit tree_split(int B, int H, int Hkv, int T) {
+  TreeSplit s;
+  s.rows = static_cast<long long>(H / Hkv) * T;
+  s.pairs = (s.rows + 255) / 256;
+  s.piece_rows = s.rows <= 128 ? 2 * s.rows : 256;
+  s.pieces = fa::kTreeMaxGrid + static_cast<long long>(B) * Hkv * s.pairs;
+  return s;
+}
+
+fa_status check_tree_sizes(int B, int H, int Hkv, int T, int d) {
+  if (B < 0 || H < 0 || T < 0)
+    return fail(FA_ERR_INVALID_ARG, "sizes must be non-negative (B=%d H=%d T=%d)", B, H, T);
+  if (d != 64 && d != 128)
+    return fail(FA_ERR_UNSUPPORTED, "head dimension d=%d is not supported (64 or 128)", d);
+  if (T > 64) return fail(FA_ERR_UNSUPPORTED, "T=%d drafted tokens (at most 64)", T);
+  if (B > fa::kTreeMaxBatch)
+    return fail(FA_ERR_UNSUPPORTED, "B=%d sequences (at most %d)", B, fa::kTreeMaxBatch);
+  if (Hkv < 0 || (H > 0 && (Hkv == 0 || H % Hkv != 0)))
+    return fail(FA_ERR_INVALID_ARG, "H=%d query heads cannot share Hkv=%d key heads", H, Hkv);
+  if (H > 65536) return fail(FA_ERR_INVALID_ARG, "H=%d heads is too large", H);
+  if (static_cast<long long>(B) * H * T >= (1ll << 31))
+    return fail(FA_ERR_INVALID_ARG, "B*H*T rows is too large");
+  return FA_OK;
+}
+
+fa_status tree_impl(const void* Q, const void* K_cache, const void* V_cache, void* O, float* LSE,
+                    const int* block_table, const int* cache_lens, const int* seqlens_q,
+                    const long long* tree_mask, int B, int H, int Hkv, int T, int num_pages,
+                    int page, int max_pages, int d, float scale, float softcap, void* workspace,
+                    size_t workspace_bytes, cudaStream_t stream) {
+  g_last_error[0] = '\0';
+  FA_TRY(check_tree_sizes(B, H, Hkv, T, d));
+  if (!(std::isfinite(scale) && scale > 0.f))
+    return fail(FA_ERR_INVALID_ARG, "scale must be finite and positive");
+  ModParams m{Hkv, softcap, nullptr, nullptr, nullptr, nullptr};
+  bool noop = false;
+  FA_TRY(check_mod(m, 0, H, 0, 0, d, scale, 0, &noop));
+  if (num_pages < 0 || max_pages < 0)
+    return fail(FA_ERR_INVALID_ARG, "num_pages and max_pages must be non-negative");
+  if (page < 8 || page > (1 << 24) || (page < 128 ? 128 % page != 0 : page % 128 != 0))
+    return fail(FA_ERR_UNSUPPORTED, "page size %d (8, 16, 32, 64 or a multiple of 128)", page);
+  if (B == 0 || H == 0 || T == 0) return FA_OK;
+  const TreeSplit sp = tree_split(B, H, Hkv, T);
+  const long long max_len = static_cast<long long>(max_pages) * page;
+  if (max_len >= (1ll << 30) ||
+      static_cast<long long>(B) * Hkv * sp.pairs > (1ll << 30) / (max_len / 128 + 1) ||
+      static_cast<long long>(num_pages) * Hkv >= (1ll << 31))
+    return fail(FA_ERR_INVALID_ARG, "the cache is too large");
+  FA_TRY(check_ptr(Q, "Q"));
+  FA_TRY(check_ptr(O, "O"));
+  if (num_pages > 0) {
+    FA_TRY(check_ptr(K_cache, "K_cache"));
+    FA_TRY(check_ptr(V_cache, "V_cache"));
+  } else if (max_pages > 0) {
+    return fail(FA_ERR_INVALID_ARG, "a block table with max_pages=%d needs pages", max_pages);
+  }
+  if (cache_lens == nullptr || (max_pages > 0 && block_table == nullptr))
+    return fail(FA_ERR_INVALID_ARG, "block_table and cache_lens are required");
+  if (!aligned4(block_table) || !aligned4(cache_lens) || !aligned4(seqlens_q) || !aligned4(LSE))
+    return fail(FA_ERR_INVALID_ARG,
+                "block_table, cache_lens, seqlens_q and LSE must be 4-byte aligned");
+  if (reinterpret_cast<uintptr_t>(tree_mask) & 7u)
+    return fail(FA_ERR_INVALID_ARG, "tree_mask is not 8-byte aligned");
+  FA_TRY(check_ptr(workspace, "workspace"));
+  const size_t need = fa_fwd_tree_workspace_bytes(B, H, Hkv, T, d);
+  if (workspace_bytes < need)
+    return fail(FA_ERR_INVALID_ARG, "workspace has %zu bytes, %zu needed", workspace_bytes,
+                need);
+  const size_t qb = static_cast<size_t>(B) * H * T * d * 2;
+  const size_t cb = static_cast<size_t>(num_pages) * Hkv * page * d * 2;
+  if (overlaps(O, qb, Q, qb) || overlaps(O, qb, K_cache, cb) || overlaps(O, qb, V_cache, cb))
+    return fail(FA_ERR_INVALID_ARG, "O overlaps an input");
+  if (overlaps(workspace, need, Q, qb) || overlaps(workspace, need, K_cache, cb) ||
+      overlaps(workspace, need, V_cache, cb) || overlaps(workspace, need, O, qb))
+    return fail(FA_ERR_INVALID_ARG, "the workspace overlaps a tensor");
+  DeviceInfo dev;
+  FA_TRY(device_info(&dev));
+  FA_TRY(require_sm100(dev));
+  fa::TreeArgs a{};
+  a.err = dev.err;
+  a.block_table = block_table;
+  a.cache_lens = cache_lens;
+  a.seqlens_q = seqlens_q;
+  a.tree_mask = reinterpret_cast<const unsigned long long*>(tree_mask);
+  a.B = B;
+  a.Hkv = Hkv;
+  a.T = T;
+  a.rows = static_cast<int>(sp.rows);
+  a.pairs = static_cast<int>(sp.pairs);
+  a.piece_rows = static_cast<int>(sp.piece_rows);
+  a.page = page;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  a.max_len = static_cast<int>(max_len);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  if (softcap > 0.f) {
+    a.cap_y = scale / softcap;
+    a.cap_log2 = static_cast<float>(1.4426950408889634 * softcap);
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const size_t slots = static_cast<size_t>(sp.pieces) * sp.piece_rows;
+  a.parts = reinterpret_cast<float*>(ws);
+  a.stats = reinterpret_cast<float2*>(ws + round256(slots * d * 4));
+  a.prefix_out = reinterpret_cast<int*>(ws + round256(slots * d * 4) + round256(slots * 8));
+  CUtensorMap tmQ, tmK, tmV;
+  FA_TRY(make_tmap(&tmQ, Q, B * Hkv, a.rows, d));
+  // (without a page there is no token to load: any valid address does)
+  const void* kc = num_pages > 0 ? K_cache : Q;
+  const void* vc = num_pages > 0 ? V_cache : Q;
+  const int box = page < 128 ? page : 128;
+  FA_TRY(make_tmap(&tmK, kc, num_pages > 0 ? num_pages * Hkv : 1, page, d, box));
+  FA_TRY(make_tmap(&tmV, vc, num_pages > 0 ? num_pages * Hkv : 1, page, d, box));
+  const int grid = dev.num_sms < fa::kTreeMaxGrid ? dev.num_sms : fa::kTreeMaxGrid;
+  cudaError_t e = fa::launch_tree_sm100(tmQ, tmK, tmV, O, LSE, a, d, grid, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "launching the tree-attention kernels");
+  return FA_OK;
+}
+
 // The start-token arrays of the packed-layout calls: both given, 4-byte aligned.
 fa_status check_cu(const int* cu_q, const int* cu_k) {
   if (cu_q == nullptr || cu_k == nullptr)
@@ -1014,6 +1229,41 @@ fa_status fa_doc_ranges(const int* doc_ids, int* doc_start, int* doc_end, int B,
   return FA_OK;
 }
 
+fa_status fa_rotary(const void* Q, void* Q_out, const void* K, void* K_out,
+                    const float* inv_freq, const int* positions, long long first, int B, int H,
+                    int Hkv, int N, int d, int R, int interleaved, int inverse, float mscale,
+                    const long long* q_strides, const long long* k_strides,
+                    cudaStream_t stream) {
+  return rotary_impl(Q, Q_out, K, K_out, inv_freq, positions, first, B, H, Hkv, N, d, R,
+                     interleaved, inverse, mscale, q_strides, k_strides, 2, stream);
+}
+
+fa_status fa_rotary_f32(const float* Q, float* Q_out, const float* K, float* K_out,
+                        const float* inv_freq, const int* positions, long long first, int B,
+                        int H, int Hkv, int N, int d, int R, int interleaved, int inverse,
+                        float mscale, const long long* q_strides, const long long* k_strides,
+                        cudaStream_t stream) {
+  return rotary_impl(Q, Q_out, K, K_out, inv_freq, positions, first, B, H, Hkv, N, d, R,
+                     interleaved, inverse, mscale, q_strides, k_strides, 4, stream);
+}
+
+size_t fa_fwd_tree_workspace_bytes(int B, int H, int Hkv, int T, int d) {
+  if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || T <= 0 || d <= 0) return 0;
+  const TreeSplit s = tree_split(B, H, Hkv, T);
+  const size_t slots = static_cast<size_t>(s.pieces) * s.piece_rows;
+  return round256(slots * d * 4) + round256(slots * 8) + round256((static_cast<size_t>(B) + 1) * 4);
+}
+
+fa_status fa_fwd_tree(const void* Q, const void* K_cache, const void* V_cache, void* O, float* LSE,
+                      const int* block_table, const int* cache_lens, const int* seqlens_q,
+                      const long long* tree_mask, int B, int H, int Hkv, int T, int num_pages,
+                      int page, int max_pages, int d, float scale, float softcap, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream) {
+  return tree_impl(Q, K_cache, V_cache, O, LSE, block_table, cache_lens, seqlens_q, tree_mask, B,
+                   H, Hkv, T, num_pages, page, max_pages, d, scale, softcap, workspace,
+                   workspace_bytes, stream);
+}
+
 fa_status fa_fwd_mod(const void* Q, const void* K, const void* V, void* O, float* LSE,
                      const float* slopes, const int* prefix, const int* doc_start,
                      const int* doc_end, int B, int H, int Hkv, int Nq, int Nk, int d,
@@ -1050,6 +1300,10 @@ fa_status fa_check_device_error(cudaStream_t stream) {
                   "a per-sequence length was negative, above the padded length, or (causal) "
                   "had more queries than keys; that sequence was skipped (error word 0x%x)",
                   word);
+    if (word & 8u)
+      return fail(FA_ERR_INVALID_ARG,
+                  "a block table named a page outside the cache; the outputs of its sequence "
+                  "are wrong (error word 0x%x)", word);
     if (word & 2u)
       return fail(FA_ERR_CUDA,
                   "a kernel found its dynamic shared memory misaligned and did no work "

@@ -104,6 +104,53 @@ cudaError_t launch_accumulate(float* acc, const void* part, void* out, long long
 cudaError_t launch_doc_ranges(const int* ids, int* start, int* end, int B, int N,
                               cudaStream_t stream);
 
+// Rotary positions of up to two tensors of heads (Q and K) over the same B*N tokens.
+// Strides are in elements; the last dimension is contiguous.
+struct RotaryTensor {
+  const void* in;
+  void* out;
+  int heads;  // 0: absent
+  long long in_b, in_h, in_n, out_b, out_h, out_n;
+};
+struct RotaryArgs {
+  RotaryTensor x[2];
+  const float* inv_freq;  // [R/2]
+  const int* positions;   // [B*N], or null: first + the token's number in its sequence
+  long long total;        // B*N
+  long long first;
+  int N, d, R;
+  int interleaved;
+  int copy_rest;  // out is another buffer: elements from R on are copied
+  float mscale, sign;
+  int tokens, heads_per_block;  // set by the launch
+};
+cudaError_t launch_rotary(const RotaryArgs& a, int elem_bytes, int num_sms, cudaStream_t stream);
+
+// Attention of few query rows per sequence over a paged cache (tree_sm100.cu).
+constexpr int kTreeMaxBatch = 4096;  // the tile-count prefix sums live in shared memory
+constexpr int kTreeMaxGrid = 148;    // CTAs of the split (one per SM of a B200)
+struct TreeArgs {
+  unsigned int* err;
+  const int* block_table;  // [B][max_pages]
+  const int* cache_lens;   // [B] cached tokens, drafted ones included
+  const int* seqlens_q;    // [B] drafted tokens, or null (all T)
+  const unsigned long long* tree_mask;  // [B][T], or null (a chain)
+  int B, Hkv, T;
+  int rows;        // T * query heads of a key head
+  int pairs;       // pairs of 128-row tiles of a key head
+  int piece_rows;  // workspace rows of one piece
+  int page, num_pages, max_pages;
+  int max_len;     // max_pages * page
+  float scale_log2, cap_y, cap_log2;
+  // workspace: [pieces][piece_rows][d] outputs, [pieces][piece_rows] (max, sum), [B + 1]
+  float* parts;
+  float2* stats;
+  int* prefix_out;
+};
+cudaError_t launch_tree_sm100(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                              const CUtensorMap& tmV, void* O, float* LSE, const TreeArgs& a,
+                              int d, int num_sms, cudaStream_t stream);
+
 // One warp waiting on an mbarrier nothing arrives on, giving up after limit_cycles with
 // the kernels' timeout error (a check of the failure path).
 cudaError_t launch_timeout_probe(long long limit_cycles, const Problem& p,

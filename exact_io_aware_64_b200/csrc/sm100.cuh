@@ -86,6 +86,7 @@ constexpr uint32_t kSpinCheck = 256;
 constexpr unsigned int kErrWaitTimeout = 1u;
 constexpr unsigned int kErrSmemAlign = 2u;
 constexpr unsigned int kErrBadLength = 4u;  // a per-sequence length out of range
+constexpr unsigned int kErrBadPage = 8u;    // a block table names a page that is not there
 
 // Wait until the phase with the given parity has completed.  Returns false if the time
 // limit runs out (then it also sets kErrWaitTimeout in *err and raises *abort so the

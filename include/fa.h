@@ -356,6 +356,77 @@ FA_API fa_status fa_bwd_mod(const void* Q, const void* K, const void* V, const v
                             size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Rotary positions of Q and K (no counterpart on the pages).  Pair k < R/2 of the first R
+ * elements of every head row is turned by the angle t = position * inv_freq[k]:
+ *   y1 = mscale (x1 cos t - x2 sin t),   y2 = mscale (x2 cos t + x1 sin t),
+ *   (x1, x2) = (x[k], x[k + R/2]), or (x[2k], x[2k+1]) when interleaved = 1;
+ * elements from R on are copied.  inverse = 1 turns by -t, which is the gradient: the
+ * gradient of the inputs is the same call on the gradient of the outputs.
+ *   Q, K       in : [B,H,N,d] and [B,Hkv,N,d]; H or Hkv = 0 leaves that tensor out
+ *   Q_out, K_out out: the same shapes; may be the input itself (same pointer and strides),
+ *                and must not overlap it otherwise, nor the other input
+ *   inv_freq   in : [R/2] float32 on the device (frequency scaling for long contexts is a
+ *                matter of its values and of mscale)
+ *   positions  in : [B,N] int32 on the device, any values; or NULL: token n of every
+ *                sequence is at position first + n
+ *   R even, 0 <= R <= d <= 512; B*N < 2^31
+ *   q_strides, k_strides: host arrays {in batch, in head, in token, out batch, out head,
+ *                out token} of strides in elements, or NULL for contiguous tensors; the
+ *                elements of a row are contiguous.  (A packed [tokens,H,d] tensor is B = 1
+ *                with strides {0, d, H*d}; a slice of a fused projection works as it is.)
+ * Angles are formed in float64 and cos and sin in float32 (fa_rotary_f32: outputs within a
+ * few float32 roundings for any position).  One kernel on `stream`; any alignment, 16-byte
+ * aligned rows run fastest.
+ */
+FA_API fa_status fa_rotary(const void* Q, void* Q_out, const void* K, void* K_out,
+                           const float* inv_freq, const int* positions, long long first, int B,
+                           int H, int Hkv, int N, int d, int R, int interleaved, int inverse,
+                           float mscale, const long long* q_strides, const long long* k_strides,
+                           cudaStream_t stream);
+FA_API fa_status fa_rotary_f32(const float* Q, float* Q_out, const float* K, float* K_out,
+                               const float* inv_freq, const int* positions, long long first,
+                               int B, int H, int Hkv, int N, int d, int R, int interleaved,
+                               int inverse, float mscale, const long long* q_strides,
+                               const long long* k_strides, cudaStream_t stream);
+
+/* Bytes of scratch that fa_fwd_tree needs (it holds the pieces of the split cache). */
+FA_API size_t fa_fwd_tree_workspace_bytes(int B, int H, int Hkv, int T, int d);
+
+/*
+ * Attention of a few query rows per sequence over a paged cache: single-token decoding
+ * (T = 1) or a tree of T drafted tokens to be verified at once (no counterpart on the
+ * pages; the definition is fa_fwd's over the keys each row sees).
+ *   Q    in : [B,H,T,d] bf16
+ *   K_cache, V_cache in : [num_pages,Hkv,page,d] bf16, H a multiple of Hkv
+ *   block_table in : [B,max_pages] int32: token j of sequence b is slot j % page of page
+ *        block_table[b][j / page]; entries behind the last token's page are not read
+ *   cache_lens in : [B] int32: cached tokens of each sequence, its drafted ones (the last
+ *        n_b, already written to the cache) included
+ *   seqlens_q in : [B] int32 or NULL: n_b, the drafted tokens of sequence b, 0 <= n_b <= T
+ *        (NULL: T); rows from n_b on are not written
+ *   tree_mask in : [B,T] int64 or NULL: bit u of row t lets drafted token t see drafted
+ *        token u (its ancestors and itself; bits from n_b on are ignored).  NULL is a
+ *        chain: token t sees drafted tokens 0 .. t.  Every row sees all tokens before
+ *        the drafted ones.
+ *   O    out: [B,H,T,d] bf16, must not overlap an input;  LSE out: [B,H,T] float32 or NULL
+ *   softcap as in fa_fwd_mod;  workspace: fa_fwd_tree_workspace_bytes bytes, 16-byte aligned
+ *   T <= 64; B <= 4096; page 8, 16, 32, 64 or a multiple of 128; d 64 or 128
+ * A row that sees no key gets O = 0 and LSE = -inf.  Slots of a page behind its sequence's
+ * end may hold anything.  A sequence whose lengths are out of range (cache_lens[b] outside
+ * [0, max_pages * page], n_b outside [0, min(T, cache_lens[b])]) is skipped, and a page
+ * number outside [0, num_pages) makes that sequence's outputs wrong; both are reported by
+ * fa_check_device_error as FA_ERR_INVALID_ARG.  Two kernels on `stream`, no atomics: the
+ * result is the same bits on every run.  Calls whose kernels may overlap need a workspace
+ * each; the contents on entry do not matter.
+ */
+FA_API fa_status fa_fwd_tree(const void* Q, const void* K_cache, const void* V_cache, void* O,
+                             float* LSE, const int* block_table, const int* cache_lens,
+                             const int* seqlens_q, const long long* tree_mask, int B, int H,
+                             int Hkv, int T, int num_pages, int page, int max_pages, int d,
+                             float scale, float softcap, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream);
+
+/*
  * Merge a partial attention result into an accumulator ("FlashAttention, simplified",
  * "The trick": the rescale-and-add step of the online softmax, applied to two results
  * over disjoint key sets, as context-parallel attention needs when each GPU holds a
