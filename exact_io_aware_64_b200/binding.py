@@ -8,6 +8,7 @@ computation runs in the library's kernels; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -24,6 +25,7 @@ FA_ERR_CUDA = 3
 FA_ERR_TIMEOUT = 4
 
 _lib = None
+_fns = {}  # the library's functions that _run has looked up
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -116,6 +118,30 @@ def _check(call: str, status: int) -> None:
 def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
+
+
+def _run(name: str, device: torch.device, stream: Optional[torch.cuda.Stream], *args) -> None:
+    """Call ``name`` on ``stream`` (default: the current stream of ``device``) with
+    ``device`` current.  The host's part of a small call takes longer than its kernel, so
+    nothing is looked up twice: the raw handle of the current stream instead of a Stream
+    object (0.2 us against 7 us), and no device change where the device is current."""
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
+    index = device.index
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device_index != index:
+        raise ValueError(f"stream is on device {stream.device_index}, the tensors on {index}")
+    else:
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, handle)
+    if st != FA_OK:
+        _check(name, st)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -447,19 +473,25 @@ def bwd_packed(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tenso
     return dQ, dK, dV
 
 
-def _check_vec(name: str, t: Optional[torch.Tensor], shape, dtype, device) -> None:
-    if t is None:
+def _check_like(name: str, t: Optional[torch.Tensor], shape: tuple, dtype, device,
+                optional: bool = False) -> None:
+    """t is a contiguous tensor of this shape, dtype and device (or None when optional)."""
+    if t is None and optional:
         return
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on the inputs' CUDA device")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    if t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
+        return
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on the inputs' device ({device}), not {t.device}")
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got "
+                     f"{t.dtype} {tuple(t.shape)}")
 
 
-def _check_device(device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on the inputs' device ({device}), not {t.device}")
+def _check_workspace(t: torch.Tensor, device) -> int:
+    if t.device != device or not t.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the inputs' device")
+    return t.numel() * t.element_size()
 
 
 def doc_ranges(doc_ids: torch.Tensor, starts: Optional[torch.Tensor] = None,
@@ -472,15 +504,13 @@ def doc_ranges(doc_ids: torch.Tensor, starts: Optional[torch.Tensor] = None,
     if doc_ids.dim() != 2:
         raise ValueError("doc_ids must have two dimensions [B, N]")
     B, N = doc_ids.shape
+    device = doc_ids.device
     _check_bhnd("doc_ids", doc_ids, (B, N), torch.int32)
     starts = torch.empty_like(doc_ids) if starts is None else starts
     ends = torch.empty_like(doc_ids) if ends is None else ends
-    _check_vec("starts", starts, (B, N), torch.int32, doc_ids.device)
-    _check_vec("ends", ends, (B, N), torch.int32, doc_ids.device)
-    with torch.cuda.device(doc_ids.device):
-        st = lib().fa_doc_ranges(_ptr(doc_ids), _ptr(starts), _ptr(ends), B, N,
-                                 _stream_handle(stream))
-    _check("fa_doc_ranges", st)
+    _check_like("starts", starts, (B, N), torch.int32, device)
+    _check_like("ends", ends, (B, N), torch.int32, device)
+    _run("fa_doc_ranges", device, stream, _ptr(doc_ids), _ptr(starts), _ptr(ends), B, N)
     return starts, ends
 
 
@@ -489,17 +519,18 @@ def _mod_shapes(Q, K, V, slopes, prefix, docs):
         raise ValueError("Q must be [B, H, Nq, d] and K, V [B, Hkv, Nk, d]")
     B, H, Nq, d = Q.shape
     Hkv, Nk = K.shape[1], K.shape[2]
+    device = Q.device
     _check_bhnd("Q", Q, (B, H, Nq, d), torch.bfloat16)
-    for name, t in (("K", K), ("V", V)):
-        _check_bhnd(name, t, (B, Hkv, Nk, d), torch.bfloat16)
-    _check_device(Q.device, K=K, V=V)
-    _check_vec("slopes", slopes, (H,), torch.float32, Q.device)
-    _check_vec("prefix", prefix, (B,), torch.int32, Q.device)
+    _check_like("K", K, (B, Hkv, Nk, d), torch.bfloat16, device)
+    _check_like("V", V, (B, Hkv, Nk, d), torch.bfloat16, device)
+    _check_like("slopes", slopes, (H,), torch.float32, device, optional=True)
+    _check_like("prefix", prefix, (B,), torch.int32, device, optional=True)
     starts, ends = (None, None) if docs is None else docs
-    _check_vec("docs[0]", starts, (B, Nk), torch.int32, Q.device)
-    _check_vec("docs[1]", ends, (B, Nk), torch.int32, Q.device)
+    if docs is not None:
+        _check_like("docs[0]", starts, (B, Nk), torch.int32, device)
+        _check_like("docs[1]", ends, (B, Nk), torch.int32, device)
     mods = (_ptr(slopes), _ptr(prefix), _ptr(starts), _ptr(ends))
-    return B, H, Hkv, Nq, Nk, d, mods
+    return B, H, Hkv, Nq, Nk, d, device, mods
 
 
 def fwd_mod(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: Optional[float] = None,
@@ -516,20 +547,19 @@ def fwd_mod(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: Optional[f
     ``docs`` = ``doc_ranges(ids)`` hides keys of other documents.  A row that sees no key
     gets O = 0 and LSE = -inf.  Returns (O, LSE); LSE is None when ``want_lse`` is False
     and none is passed."""
-    B, H, Hkv, Nq, Nk, d, mods = _mod_shapes(Q, K, V, slopes, prefix, docs)
+    B, H, Hkv, Nq, Nk, d, device, mods = _mod_shapes(Q, K, V, slopes, prefix, docs)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    O = torch.empty_like(Q) if O is None else O
-    _check_bhnd("O", O, (B, H, Nq, d), torch.bfloat16)
-    if LSE is None and want_lse:
-        LSE = torch.empty((B, H, Nq), device=Q.device, dtype=torch.float32)
-    _check_vec("LSE", LSE, (B, H, Nq), torch.float32, Q.device)
-    _check_device(Q.device, O=O)
-    with torch.cuda.device(Q.device):
-        st = lib().fa_fwd_mod(_ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(LSE), *mods, B, H, Hkv,
-                              Nq, Nk, d, float(scale), int(bool(causal)), float(softcap),
-                              _stream_handle(stream))
-    _check("fa_fwd_mod", st)
+    if O is None:
+        O = torch.empty_like(Q)
+    else:
+        _check_like("O", O, (B, H, Nq, d), torch.bfloat16, device)
+    if LSE is not None:
+        _check_like("LSE", LSE, (B, H, Nq), torch.float32, device)
+    elif want_lse:
+        LSE = torch.empty((B, H, Nq), device=device, dtype=torch.float32)
+    _run("fa_fwd_mod", device, stream, _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(LSE), *mods, B,
+         H, Hkv, Nq, Nk, d, float(scale), int(bool(causal)), float(softcap))
     return O, LSE
 
 
@@ -543,31 +573,26 @@ def bwd_mod(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tensor,
     """Backward of ``fwd_mod`` with the same modifications through ``fa_bwd_mod``.  dK and
     dV [B, Hkv, Nk, d] are summed over the query heads that share a key head; slopes are
     constants.  Every row of every gradient is written.  Returns (dQ, dK, dV)."""
-    B, H, Hkv, Nq, Nk, d, mods = _mod_shapes(Q, K, V, slopes, prefix, docs)
-    for name, t in (("O", O), ("dO", dO)):
-        _check_bhnd(name, t, (B, H, Nq, d), torch.bfloat16)
-    _check_bhnd("LSE", LSE, (B, H, Nq), torch.float32)
+    B, H, Hkv, Nq, Nk, d, device, mods = _mod_shapes(Q, K, V, slopes, prefix, docs)
+    q_shape, k_shape = (B, H, Nq, d), (B, Hkv, Nk, d)
+    _check_like("O", O, q_shape, torch.bfloat16, device)
+    _check_like("dO", dO, q_shape, torch.bfloat16, device)
+    _check_like("LSE", LSE, (B, H, Nq), torch.float32, device)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     dQ = torch.empty_like(Q) if dQ is None else dQ
     dK = torch.empty_like(K) if dK is None else dK
     dV = torch.empty_like(V) if dV is None else dV
-    _check_bhnd("dQ", dQ, (B, H, Nq, d), torch.bfloat16)
-    for name, t in (("dK", dK), ("dV", dV)):
-        _check_bhnd(name, t, (B, Hkv, Nk, d), torch.bfloat16)
+    _check_like("dQ", dQ, q_shape, torch.bfloat16, device)
+    _check_like("dK", dK, k_shape, torch.bfloat16, device)
+    _check_like("dV", dV, k_shape, torch.bfloat16, device)
     if workspace is None:
-        workspace = torch.empty(max(workspace_bytes(B, H, Nq, d), 16), device=Q.device,
+        workspace = torch.empty(max(workspace_bytes(B, H, Nq, d), 16), device=device,
                                 dtype=torch.uint8)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _check_device(Q.device, O=O, dO=dO, LSE=LSE, dQ=dQ, dK=dK, dV=dV, workspace=workspace)
-    ws_bytes = workspace.numel() * workspace.element_size()
-    with torch.cuda.device(Q.device):
-        st = lib().fa_bwd_mod(_ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(dO), _ptr(LSE), _ptr(dQ),
-                              _ptr(dK), _ptr(dV), *mods, B, H, Hkv, Nq, Nk, d, float(scale),
-                              int(bool(causal)), float(softcap), _ptr(workspace), ws_bytes,
-                              _stream_handle(stream))
-    _check("fa_bwd_mod", st)
+    ws_bytes = _check_workspace(workspace, device)
+    _run("fa_bwd_mod", device, stream, _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(dO), _ptr(LSE),
+         _ptr(dQ), _ptr(dK), _ptr(dV), *mods, B, H, Hkv, Nq, Nk, d, float(scale),
+         int(bool(causal)), float(softcap), _ptr(workspace), ws_bytes)
     return dQ, dK, dV
 
 
@@ -608,21 +633,24 @@ def rotary_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0,
 
 
 def _rotary_side(name, x, out, dtype, device):
-    """(B, heads, N, d) and the stride array of one tensor of a rotary call."""
+    """(B, heads, N, d) and the stride array of one tensor of a rotary call; None for the
+    strides of contiguous [B, heads, N, d] tensors."""
     for what, t in ((name, x), (f"{name}'s output", out)):
-        if not t.is_cuda or t.device != device:
-            raise ValueError(f"{what} must be on the inputs' CUDA device")
-        if t.dtype != dtype:
-            raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+        if t.dtype != dtype or t.device != device or not t.is_cuda:
+            raise ValueError(f"{what} must be a {dtype} CUDA tensor on {device}, got {t.dtype} "
+                             f"on {t.device}")
         if t.dim() not in (3, 4) or t.shape != x.shape:
             raise ValueError(f"{what} must be [B, heads, N, d] or packed [tokens, heads, d]")
+    if x.dim() == 4 and x.is_contiguous() and out.is_contiguous():
+        return x.shape, None
+    for what, t in ((name, x), (f"{name}'s output", out)):
         if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
             raise ValueError(f"{what} must be contiguous in its last dimension")
     if x.dim() == 3:
         N, heads, d = x.shape
         st = [0, x.stride(1), x.stride(0), 0, out.stride(1), out.stride(0)]
         return (1, heads, N, d), (_ll * 6)(*st)
-    return tuple(x.shape), (_ll * 6)(*x.stride()[:3], *out.stride()[:3])
+    return x.shape, (_ll * 6)(*x.stride()[:3], *out.stride()[:3])
 
 
 def _rotary(Q, K, inv_freq, positions, first, interleaved, mscale, Q_out, K_out, inverse, stream):
@@ -640,17 +668,12 @@ def _rotary(Q, K, inv_freq, positions, first, interleaved, mscale, Q_out, K_out,
     elif K_out is not None:
         raise ValueError("K_out without K")
     R = 2 * inv_freq.numel()
-    _check_vec("inv_freq", inv_freq, (R // 2,), torch.float32, device)
+    _check_like("inv_freq", inv_freq, (R // 2,), torch.float32, device)
     if positions is not None:
-        shape = (N,) if Q.dim() == 3 else (B, N)
-        _check_vec("positions", positions, shape, torch.int32, device)
-    name = "fa_rotary" if dtype == torch.bfloat16 else "fa_rotary_f32"
-    with torch.cuda.device(device):
-        st = getattr(lib(), name)(_ptr(Q), _ptr(Q_out), _ptr(K), _ptr(K_out), _ptr(inv_freq),
-                                  _ptr(positions), int(first), B, H, Hkv, N, d, R,
-                                  int(bool(interleaved)), int(inverse), float(mscale), qs, ks,
-                                  _stream_handle(stream))
-    _check(name, st)
+        _check_like("positions", positions, (N,) if Q.dim() == 3 else (B, N), torch.int32, device)
+    _run("fa_rotary" if dtype == torch.bfloat16 else "fa_rotary_f32", device, stream, _ptr(Q),
+         _ptr(Q_out), _ptr(K), _ptr(K_out), _ptr(inv_freq), _ptr(positions), int(first), B, H,
+         Hkv, N, d, R, int(bool(interleaved)), inverse, float(mscale), qs, ks)
     return Q_out, K_out
 
 
@@ -678,6 +701,7 @@ def rotary_bwd(dQ_out: torch.Tensor, dK_out: Optional[torch.Tensor], inv_freq: t
                    stream)
 
 
+@functools.lru_cache(maxsize=256)
 def tree_workspace_bytes(B: int, H: int, Hkv: int, T: int, d: int) -> int:
     return int(lib().fa_fwd_tree_workspace_bytes(B, H, Hkv, T, d))
 
@@ -705,37 +729,33 @@ def fwd_tree(Q: torch.Tensor, K_cache: torch.Tensor, V_cache: torch.Tensor,
     B, H, T, d = Q.shape
     num_pages, Hkv, page, _ = K_cache.shape
     max_pages = block_table.shape[1]
+    device = Q.device
+    cache = (num_pages, Hkv, page, d)
     _check_bhnd("Q", Q, (B, H, T, d), torch.bfloat16)
-    for name, t in (("K_cache", K_cache), ("V_cache", V_cache)):
-        _check_bhnd(name, t, (num_pages, Hkv, page, d), torch.bfloat16)
-    _check_device(Q.device, K_cache=K_cache, V_cache=V_cache)
-    _check_vec("block_table", block_table, (B, max_pages), torch.int32, Q.device)
-    _check_vec("cache_lens", cache_lens, (B,), torch.int32, Q.device)
-    _check_vec("seqlens_q", seqlens_q, (B,), torch.int32, Q.device)
-    _check_vec("tree_mask", tree_mask, (B, T), torch.int64, Q.device)
+    _check_like("K_cache", K_cache, cache, torch.bfloat16, device)
+    _check_like("V_cache", V_cache, cache, torch.bfloat16, device)
+    _check_like("block_table", block_table, (B, max_pages), torch.int32, device)
+    _check_like("cache_lens", cache_lens, (B,), torch.int32, device)
+    _check_like("seqlens_q", seqlens_q, (B,), torch.int32, device, optional=True)
+    _check_like("tree_mask", tree_mask, (B, T), torch.int64, device, optional=True)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if O is None:
         O = torch.empty_like(Q) if seqlens_q is None else torch.zeros_like(Q)
-    _check_bhnd("O", O, (B, H, T, d), torch.bfloat16)
-    if LSE is None and want_lse:
-        LSE = torch.full((B, H, T), float("-inf"), device=Q.device) if seqlens_q is not None \
-            else torch.empty((B, H, T), device=Q.device, dtype=torch.float32)
-    _check_vec("LSE", LSE, (B, H, T), torch.float32, Q.device)
+    else:
+        _check_like("O", O, (B, H, T, d), torch.bfloat16, device)
+    if LSE is not None:
+        _check_like("LSE", LSE, (B, H, T), torch.float32, device)
+    elif want_lse:
+        LSE = torch.empty((B, H, T), device=device, dtype=torch.float32) if seqlens_q is None \
+            else torch.full((B, H, T), float("-inf"), device=device)
     if workspace is None:
-        workspace = torch.empty(max(tree_workspace_bytes(B, H, Hkv, T, d), 16), device=Q.device,
+        workspace = torch.empty(max(tree_workspace_bytes(B, H, Hkv, T, d), 16), device=device,
                                 dtype=torch.uint8)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _check_device(Q.device, O=O, workspace=workspace)
-    ws_bytes = workspace.numel() * workspace.element_size()
-    with torch.cuda.device(Q.device):
-        st = lib().fa_fwd_tree(_ptr(Q), _ptr(K_cache), _ptr(V_cache), _ptr(O), _ptr(LSE),
-                               _ptr(block_table), _ptr(cache_lens), _ptr(seqlens_q),
-                               _ptr(tree_mask), B, H, Hkv, T, num_pages, page, max_pages, d,
-                               float(scale), float(softcap), _ptr(workspace), ws_bytes,
-                               _stream_handle(stream))
-    _check("fa_fwd_tree", st)
+    ws_bytes = _check_workspace(workspace, device)
+    _run("fa_fwd_tree", device, stream, _ptr(Q), _ptr(K_cache), _ptr(V_cache), _ptr(O), _ptr(LSE),
+         _ptr(block_table), _ptr(cache_lens), _ptr(seqlens_q), _ptr(tree_mask), B, H, Hkv, T,
+         num_pages, page, max_pages, d, float(scale), float(softcap), _ptr(workspace), ws_bytes)
     return O, LSE
 
 

@@ -1348,24 +1348,15 @@ cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   a_q.total_units = p.BH * a.n_qt;
   const int grid_kv = a_kv.total_units < num_sms ? a_kv.total_units : num_sms;
   const int grid_q = a_q.total_units < num_sms ? a_q.total_units : num_sms;
-  // the in-kernel register split assumes exactly kRegsLaunch registers a thread at launch
-  cudaFuncAttributes fattr;
-  e = cudaFuncGetAttributes(&fattr, bwd_dkdv_kernel<D, kMode>);
+  static std::atomic<uint64_t> ready_kv{0}, ready_q{0};
+  e = ready_kernel(bwd_dkdv_kernel<D, kMode>, kRegsLaunch, DkdvLayout<D>::kAlloc, ready_kv);
   if (e != cudaSuccess) return e;
-  if (fattr.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-  e = cudaFuncGetAttributes(&fattr, bwd_dq_kernel<D, kMode>);
-  if (e != cudaSuccess) return e;
-  if (fattr.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(bwd_dkdv_kernel<D, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           DkdvLayout<D>::kAlloc);
+  e = ready_kernel(bwd_dq_kernel<D, kMode>, kRegsLaunch, DqLayout<D>::kAlloc, ready_q);
   if (e != cudaSuccess) return e;
   bwd_dkdv_kernel<D, kMode><<<grid_kv, kThreads, DkdvLayout<D>::kAlloc, stream>>>(
       tmQ, tmK, tmV, tmdO, tmL2, tmD, tmdK, tmdV, a_kv);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = trace_mark(p, 2, stream)) != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(bwd_dq_kernel<D, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           DqLayout<D>::kAlloc);
-  if (e != cudaSuccess) return e;
   bwd_dq_kernel<D, kMode><<<grid_q, kThreads, DqLayout<D>::kAlloc, stream>>>(tmQ, tmK, tmV, tmdO, a_q);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return trace_mark(p, 3, stream);

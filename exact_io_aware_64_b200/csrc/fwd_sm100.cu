@@ -836,14 +836,8 @@ cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   a.total_units = p.BH * a.n_units;
   a.scale_log2 = p.scale * kLog2e;
   a.mod = mod_args(p);
-  // The register split inside the kernel assumes exactly kRegsLaunch registers a thread
-  // at launch; with fewer, the softmax warpgroups' increase could never be granted.
-  cudaFuncAttributes fattr;
-  cudaError_t e = cudaFuncGetAttributes(&fattr, fwd_sm100_kernel<D, kMode>);
-  if (e != cudaSuccess) return e;
-  if (fattr.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(fwd_sm100_kernel<D, kMode>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = ready_kernel(fwd_sm100_kernel<D, kMode>, kRegsLaunch, L::kAlloc, ready);
   if (e != cudaSuccess) return e;
   const int grid = a.total_units < num_sms ? a.total_units : num_sms;
   if ((e = trace_mark(p, 0, stream)) != cudaSuccess) return e;

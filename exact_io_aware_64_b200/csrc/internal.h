@@ -4,9 +4,31 @@
 
 #include <cuda.h>
 #include <cuda_runtime_api.h>
+#include <atomic>
 #include <cstddef>
+#include <cstdint>
 
 namespace fa {
+
+// What a tensor-core kernel needs once per device before its first launch there: the
+// dynamic shared memory it asks for allowed, and its register count checked (the register
+// split inside assumes exactly `regs` a thread at launch; with fewer, the increases could
+// never be granted).  `done` holds a bit per device.
+template <typename Kernel>
+cudaError_t ready_kernel(Kernel* kernel, int regs, int smem, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaFuncAttributes fattr;
+  if ((e = cudaFuncGetAttributes(&fattr, kernel)) != cudaSuccess) return e;
+  if (fattr.numRegs != regs) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  done.fetch_or(bit, std::memory_order_release);
+  return cudaSuccess;
+}
 
 // Problem shared by every kernel: [B*H, N, d] query-side tensors (Q, O, dO, dQ, LSE)
 // and [B*H, Nk, d] key-side tensors (K, V, dK, dV), contiguous.  Nk == N except for

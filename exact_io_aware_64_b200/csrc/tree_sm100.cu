@@ -599,13 +599,8 @@ template <int D, bool kCap>
 cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                      void* O, float* LSE, const TreeArgs& a, int num_sms, cudaStream_t stream) {
   auto* kernel = tree_sm100_kernel<D, kCap>;
-  // the in-kernel register split assumes exactly kRegsLaunch registers a thread at launch
-  cudaFuncAttributes fattr;
-  cudaError_t e = cudaFuncGetAttributes(&fattr, kernel);
-  if (e != cudaSuccess) return e;
-  if (fattr.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Layout<D>::bytes(a.B));
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = ready_kernel(kernel, kRegsLaunch, Layout<D>::bytes(kTreeMaxBatch), ready);
   if (e != cudaSuccess) return e;
   kernel<<<num_sms, kThreads, Layout<D>::bytes(a.B), stream>>>(tmQ, tmK, tmV, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
