@@ -646,8 +646,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int delta = (j - i) * kTile - off;
           const bool diag = args.causal && delta > -kTile;
           const uint64_t scale2 = f32x2(args.scale_log2, args.scale_log2);
-          const float unit = kMode == kModCap ? args.mod.cap_log2 : args.scale_log2;
-          const uint64_t unit2 = f32x2(unit, unit);
           bool masked = false, straddles = false;
           int mlo = 0;
           unsigned width = 0;
@@ -672,41 +670,42 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t pk[kCols / 4];
-            float th[kCols / 2];  // with a cap: tanh of this half's scores
+            int form = kCapTanh;
             if constexpr (kMode == kModCap) {
+              float raw[kCols / 2];
 #pragma unroll
-              for (int c = 0; c < kCols / 2; ++c)
-                th[c] = __uint_as_float(r[hf * (kCols / 2) + c]);
-              tanh_scores<kCols / 2>(th, args.mod);
+              for (int c = 0; c < kCols / 2; ++c) raw[c] = __uint_as_float(r[hf * (kCols / 2) + c]);
+              form = cap_form(abs_max<kCols / 2>(raw), args.mod.cap);
             }
+            with_cap_form<kMode>(form, [&](auto f) {
 #pragma unroll
-            for (int c = hf * (kCols / 2); c < (hf + 1) * (kCols / 2); c += 2) {
-              // x = S^T * scale * log2e - L2 for two query columns in one packed FMA
-              const uint64_t nl = *reinterpret_cast<const uint64_t*>(sL + c);
-              float e0, e1;
-              if constexpr (kMode == kModNone) {
-                const uint64_t x2 =
-                    fma_x2(f32x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), scale2, nl);
-                exp2_pair(x2, e0, e1);
-                if (diag && col0 + c < row + delta) e0 = 0.f;
-                if (diag && col0 + c + 1 < row + delta) e1 = 0.f;
-                p[c] = e0;
-                p[c + 1] = e1;
-              } else {
-                float g0, g1;
-                const int k = c - hf * (kCols / 2);
-                mod_prob_pair<kMode>(kMode == kModCap ? th[k] : __uint_as_float(r[c]),
-                                     kMode == kModCap ? th[k + 1] : __uint_as_float(r[c + 1]),
-                                     args.mod, unit2, nl, sl, pos_d + static_cast<float>(c), straddles,
-                                     e0, e1, g0, g1);
-                if (masked && static_cast<unsigned>(c - mlo) >= width) e0 = 0.f;
-                if (masked && static_cast<unsigned>(c + 1 - mlo) >= width) e1 = 0.f;
-                pk[k / 2] = pack_bf16x2(e0, e1);
-                // dS carries the cap's derivative
-                p[c] = kMode == kModCap ? e0 * g0 : e0;
-                p[c + 1] = kMode == kModCap ? e1 * g1 : e1;
+              for (int c = hf * (kCols / 2); c < (hf + 1) * (kCols / 2); c += 2) {
+                // x = S^T * scale * log2e - L2 for two query columns in one packed FMA
+                const uint64_t nl = *reinterpret_cast<const uint64_t*>(sL + c);
+                float e0, e1;
+                if constexpr (kMode == kModNone) {
+                  const uint64_t x2 =
+                      fma_x2(f32x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), scale2, nl);
+                  exp2_pair(x2, e0, e1);
+                  if (diag && col0 + c < row + delta) e0 = 0.f;
+                  if (diag && col0 + c + 1 < row + delta) e1 = 0.f;
+                  p[c] = e0;
+                  p[c + 1] = e1;
+                } else {
+                  float g0, g1;
+                  mod_prob_pair<kMode, f.value>(__uint_as_float(r[c]), __uint_as_float(r[c + 1]),
+                                                args.mod, scale2, nl, sl,
+                                                pos_d + static_cast<float>(c), straddles, e0, e1,
+                                                g0, g1);
+                  if (masked && static_cast<unsigned>(c - mlo) >= width) e0 = 0.f;
+                  if (masked && static_cast<unsigned>(c + 1 - mlo) >= width) e1 = 0.f;
+                  pk[c / 2 - hf * (kCols / 4)] = pack_bf16x2(e0, e1);
+                  // dS carries the cap's derivative
+                  p[c] = kMode == kModCap ? e0 * g0 : e0;
+                  p[c + 1] = kMode == kModCap ? e1 * g1 : e1;
+                }
               }
-            }
+            });
             if constexpr (kMode == kModNone) {
 #pragma unroll
               for (int c = 0; c < kCols / 4; ++c)
@@ -1208,22 +1207,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool before = kv0 + kCols - 1 <= pos0, after = kv0 >= pos0 + kTile - 1;
             const float sl = before ? slope2 : -slope2;
             const float pos_d = static_cast<float>(kv0 - (q_row + off));
-            const float unit = kMode == kModCap ? args.mod.cap_log2 : args.scale_log2;
-            const uint64_t unit2 = f32x2(unit, unit);
-            float x[kCols];
+            int form = kCapTanh;
+            if constexpr (kMode == kModCap) {
+              float raw[kCols];
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) x[c] = __uint_as_float(r[c]);
-            if constexpr (kMode == kModCap) tanh_scores<kCols>(x, args.mod);
-#pragma unroll
-            for (int c = 0; c < kCols; c += 2) {
-              float e0, e1, g0, g1;
-              mod_prob_pair<kMode>(x[c], x[c + 1], args.mod, unit2, nl2, sl, pos_d + static_cast<float>(c),
-                                   !before && !after, e0, e1, g0, g1);
-              if (masked && static_cast<unsigned>(c - mlo) >= width) e0 = 0.f;
-              if (masked && static_cast<unsigned>(c + 1 - mlo) >= width) e1 = 0.f;
-              p[c] = kMode == kModCap ? e0 * g0 : e0;
-              p[c + 1] = kMode == kModCap ? e1 * g1 : e1;
+              for (int c = 0; c < kCols; ++c) raw[c] = __uint_as_float(r[c]);
+              form = cap_form(abs_max<kCols>(raw), args.mod.cap);
             }
+            with_cap_form<kMode>(form, [&](auto f) {
+#pragma unroll
+              for (int c = 0; c < kCols; c += 2) {
+                float e0, e1, g0, g1;
+                mod_prob_pair<kMode, f.value>(__uint_as_float(r[c]), __uint_as_float(r[c + 1]),
+                                              args.mod, scale2, nl2, sl,
+                                              pos_d + static_cast<float>(c), !before && !after, e0,
+                                              e1, g0, g1);
+                if (masked && static_cast<unsigned>(c - mlo) >= width) e0 = 0.f;
+                if (masked && static_cast<unsigned>(c + 1 - mlo) >= width) e1 = 0.f;
+                p[c] = kMode == kModCap ? e0 * g0 : e0;
+                p[c + 1] = kMode == kModCap ? e1 * g1 : e1;
+              }
+            });
           } else {
 #pragma unroll
           for (int c = 0; c < kCols; c += 2) {

@@ -4,12 +4,12 @@
 //   end[j]   = one past its last token;  start[j] = end[j] = j for padding (id < 0).
 //
 // start is a running maximum of (j where a run begins) from the left, end a running
-// minimum of (j + 1 where a run ends) from the right.  One CTA per sequence walks chunks
-// of 8192 tokens, 8 to a thread: a scan over the thread's own tokens, one over the
-// threads (shuffles inside a warp, then over the 32 warps), and a carry from chunk to
-// chunk.  12 bytes per token in all; a call is bound by the latency of its two passes
-// (a few microseconds), is made once per batch, and serves every layer's forward and
-// backward calls.
+// minimum of (j + 1 where a run ends) from the right.  A CTA takes 2048 tokens, 4 to a
+// thread: a scan over the thread's own, one over the threads (shuffles inside a warp, then
+// over the warps), and for the runs that cross the chunk's ends a search outwards, 4096
+// tokens a step by the whole block, up to the run's own end.  12 bytes a token: a call is
+// bound by the latency of a few dependent loads, is made once per batch, and serves every
+// layer's forward and backward calls.
 #include <climits>
 
 #include "internal.h"
@@ -17,9 +17,11 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kPer = 8;  // tokens per thread and chunk
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kPer = 4;  // tokens per thread
 constexpr int kChunk = kThreads * kPer;
+constexpr int kSearch = 8;  // tokens per thread and search step
 
 struct Max {
   static constexpr int identity = -1;
@@ -31,9 +33,9 @@ struct Min {
 };
 
 // Exclusive scan of one value per thread over the block, in thread order (or, reversed,
-// from the last thread down); `total` becomes the scan over all threads.
+// from the last thread down).
 template <class Op, bool kReverse>
-__device__ int block_scan(int v, int* warp_val, int& total) {
+__device__ int block_scan(int v, int* warp_val) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const unsigned all = 0xffffffffu;
   int x = v;
@@ -45,76 +47,108 @@ __device__ int block_scan(int v, int* warp_val, int& total) {
   __syncthreads();  // the previous scan's readers are done with warp_val
   if (lane == (kReverse ? 0 : 31)) warp_val[warp] = x;
   __syncthreads();
-  int w = warp_val[lane];
+  int w = lane < kWarps ? warp_val[lane] : Op::identity;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = kReverse ? __shfl_down_sync(all, w, o) : __shfl_up_sync(all, w, o);
     if (kReverse ? lane + o < 32 : lane >= o) w = Op::op(w, y);
   }
-  total = __shfl_sync(all, w, kReverse ? 0 : 31);
   const int before = __shfl_sync(all, w, kReverse ? min(warp + 1, 31) : max(warp - 1, 0));
   int ex = kReverse ? __shfl_down_sync(all, x, 1) : __shfl_up_sync(all, x, 1);
   if (lane == (kReverse ? 31 : 0)) ex = Op::identity;
-  if (warp != (kReverse ? 31 : 0)) ex = Op::op(ex, before);
+  if (warp != (kReverse ? kWarps - 1 : 0)) ex = Op::op(ex, before);
   return ex;
+}
+
+// The scan of every thread's v over the whole block.
+template <class Op>
+__device__ int block_all(int v, int* warp_val) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = Op::op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) warp_val[threadIdx.x / 32] = v;
+  __syncthreads();
+  v = warp_val[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) v = Op::op(v, warp_val[w]);
+  return v;
 }
 
 __global__ void __launch_bounds__(kThreads)
     doc_ranges_kernel(const int* __restrict__ ids, int* __restrict__ start,
                       int* __restrict__ end, int N) {
-  __shared__ int warp_val[32];
-  const size_t row = static_cast<size_t>(blockIdx.x) * N;
+  __shared__ int warp_val[kWarps];
+  const size_t row = static_cast<size_t>(blockIdx.y) * N;
   ids += row;
   start += row;
   end += row;
   auto id_at = [&](int j) { return j >= 0 && j < N ? max(ids[j], -1) : -2; };
-  int carry = Max::identity;
-  for (int c = 0; c < N; c += kChunk) {
-    const int j0 = c + static_cast<int>(threadIdx.x) * kPer;
-    int id[kPer + 1];
+  const int c0 = blockIdx.x * kChunk, c1 = min(c0 + kChunk, N);
+  const int j0 = c0 + static_cast<int>(threadIdx.x) * kPer;
+  int id[kPer + 2];  // tokens j0 - 1 .. j0 + kPer
 #pragma unroll
-    for (int k = 0; k <= kPer; ++k) id[k] = id_at(j0 + k - 1);
-    int v[kPer];
-    int run = Max::identity;
+  for (int k = 0; k < kPer + 2; ++k) id[k] = id_at(j0 + k - 1);
+  // first token of the run that enters the chunk, one past the last of the one that leaves
+  int left = c0, right = c1;
+  const int first = id_at(c0), last = id_at(c1 - 1);
+  if (first >= 0 && id_at(c0 - 1) == first) {
+    left = Max::identity;
+    for (int top = c0 - 1; left < 0; top -= kThreads * kSearch) {
+      int found = Max::identity;  // (token 0 begins a run: the search ends there)
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      if (id[k + 1] != id[k]) run = j0 + k;
-      v[k] = run;
+      for (int k = 0; k < kSearch; ++k) {
+        const int j = top - k * kThreads - static_cast<int>(threadIdx.x);
+        if (j >= 0 && (j == 0 || ids[j - 1] != ids[j])) found = max(found, j);
+      }
+      left = block_all<Max>(found, warp_val);
     }
-    int total;
-    const int before = max(block_scan<Max, false>(run, warp_val, total), carry);
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      if (j0 + k < N) start[j0 + k] = id[k + 1] < 0 ? j0 + k : max(v[k], before);
-    carry = max(carry, total);
   }
-  carry = Min::identity;
-  for (int c = (N - 1) / kChunk * kChunk; c >= 0; c -= kChunk) {
-    const int j0 = c + static_cast<int>(threadIdx.x) * kPer;
-    int id[kPer + 1];
+  if (last >= 0 && id_at(c1) == last) {
+    right = Min::identity;
+    for (int low = c1; right == Min::identity; low += kThreads * kSearch) {
+      int found = Min::identity;
 #pragma unroll
-    for (int k = 0; k <= kPer; ++k) id[k] = id_at(j0 + k);
-    int v[kPer];
-    int run = Min::identity;
-#pragma unroll
-    for (int k = kPer - 1; k >= 0; --k) {
-      if (j0 + k < N && id[k] != id[k + 1]) run = j0 + k + 1;
-      v[k] = run;
+      for (int k = 0; k < kSearch; ++k) {
+        const int j = low + k * kThreads + static_cast<int>(threadIdx.x);
+        if (j < N && (j == N - 1 || ids[j + 1] != ids[j])) found = min(found, j + 1);
+      }
+      right = block_all<Min>(found, warp_val);
     }
-    int total;
-    const int after = min(block_scan<Min, true>(run, warp_val, total), carry);
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      if (j0 + k < N) end[j0 + k] = id[k] < 0 ? j0 + k : min(v[k], after);
-    carry = min(carry, total);
   }
+  int v[kPer];
+  int run = Max::identity;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (j0 + k < c1 && id[k + 1] != id[k]) run = j0 + k;
+    v[k] = run;
+  }
+  const int before = max(block_scan<Max, false>(run, warp_val), left);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k)
+    if (j0 + k < c1) start[j0 + k] = id[k + 1] < 0 ? j0 + k : max(v[k], before);
+  run = Min::identity;
+#pragma unroll
+  for (int k = kPer - 1; k >= 0; --k) {
+    if (j0 + k < c1 && id[k + 1] != id[k + 2]) run = j0 + k + 1;
+    v[k] = run;
+  }
+  const int after = min(block_scan<Min, true>(run, warp_val), right);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k)
+    if (j0 + k < c1) end[j0 + k] = id[k + 1] < 0 ? j0 + k : min(v[k], after);
 }
 
 }  // namespace
 
 cudaError_t launch_doc_ranges(const int* ids, int* start, int* end, int B, int N,
                               cudaStream_t stream) {
-  doc_ranges_kernel<<<B, kThreads, 0, stream>>>(ids, start, end, N);
+  // (a grid's y extent is limited: rows in slices)
+  for (int b = 0; b < B; b += 65535) {
+    const dim3 grid(static_cast<unsigned>((N + kChunk - 1) / kChunk),
+                    static_cast<unsigned>(B - b < 65535 ? B - b : 65535));
+    const size_t at = static_cast<size_t>(b) * N;
+    doc_ranges_kernel<<<grid, kThreads, 0, stream>>>(ids + at, start + at, end + at, N);
+  }
   return cudaGetLastError();
 }
 

@@ -410,8 +410,8 @@ fa_status check_mod(const ModParams& m, int B, int H, int Nq, int Nk, int d, flo
     return fail(FA_ERR_INVALID_ARG, "H=%d query heads cannot share Hkv=%d key heads", H, m.Hkv);
   if (!(std::isfinite(m.softcap) && m.softcap >= 0.f))
     return fail(FA_ERR_INVALID_ARG, "softcap must be finite and non-negative (0: no cap)");
-  if (m.softcap > 0.f && !(scale / m.softcap < 1e30f && m.softcap < 1e30f &&
-                           scale / m.softcap > 1e-30f))
+  if (m.softcap > 0.f && !(m.softcap > 1e-9f && m.softcap < 1e9f && scale / m.softcap > 1e-12f &&
+                           scale / m.softcap < 1e12f))
     return fail(FA_ERR_INVALID_ARG, "softcap %g is out of range for scale %g",
                 static_cast<double>(m.softcap), static_cast<double>(scale));
   if (m.prefix != nullptr && !causal)
@@ -727,11 +727,9 @@ fa_status tree_impl(const void* Q, const void* K_cache, const void* V_cache, voi
   a.num_pages = num_pages;
   a.max_pages = max_pages;
   a.max_len = static_cast<int>(max_len);
+  a.scale = scale;
   a.scale_log2 = scale * 1.4426950408889634f;
-  if (softcap > 0.f) {
-    a.cap_y = scale / softcap;
-    a.cap_log2 = static_cast<float>(1.4426950408889634 * softcap);
-  }
+  a.softcap = softcap;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const size_t slots = static_cast<size_t>(sp.pieces) * sp.piece_rows;
   a.parts = reinterpret_cast<float*>(ws);

@@ -600,11 +600,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kBN; ++c) s[c] = __uint_as_float(sr[c]);
         const int kv0 = (ui.jb + j) * kBN;
         // log2-unit score of entry c: s[c] * unit + shift
+        // (with a cap and form kCap3 or kCap5, s[c] q(s[c]^2) instead)
         float unit = args.scale_log2, shift = 0.f;
+        int form = kCapTanh;
         if constexpr (kMode != kModNone) {
+          const bool partial = kv0 < full_lo || kv0 + kBN > full_hi;
           if constexpr (kMode == kModCap) {
-            tanh_scores<kBN>(s, args.mod);
-            unit = args.mod.cap_log2;
+            if (partial || slope2 != 0.f || (form = cap_form(abs_max<kBN>(s), args.mod.cap)) == kCapTanh) {
+              cap_scores<kBN>(s, args.mod.cap);
+              unit = 1.f;
+              form = kCapTanh;
+            }
           }
           if (slope2 != 0.f) {
             // -slope |p - j|, p the row's position: linear in the key inside a tile that
@@ -629,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             unit = 1.f;
           }
-          if (kv0 < full_lo || kv0 + kBN > full_hi) {
+          if (partial) {
             const int lo = lim_row.lo - kv0;
             const unsigned width = static_cast<unsigned>(lim_row.hi - lim_row.lo);
 #pragma unroll
@@ -657,7 +663,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 8; c < kBN; c += 2) mx8[(c / 2) % 8] = max3(mx8[(c / 2) % 8], s[c], s[c + 1]);
         const float mx = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]),
                               fmaxf(mx8[6], mx8[7]));
-        const float m_tile = kMode == kModNone ? mx * args.scale_log2 : fmaf(mx, unit, shift);
+        float m_tile = kMode == kModNone ? mx * args.scale_log2 : fmaf(mx, unit, shift);
+        // (the cap rises, so the largest product has the largest score)
+        if (kMode == kModCap && form != kCapTanh) m_tile = args.mod.cap.out * cap_tanh(mx, args.mod.cap);
         float alpha = 1.f;
         bool rescale = false;
         if (m_tile > m + kRescaleThreshold || m == -INFINITY) {
@@ -697,14 +705,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t scale2 = f32x2(sc, sc);
         const uint64_t negm2 = f32x2(negm, negm);
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
+        with_cap_form<kMode>(form, [&](auto f) {
 #pragma unroll
-        for (int c = 0; c < kBN / 2; ++c) {
-          const uint64_t x2 = fma_x2(f32x2(s[2 * c], s[2 * c + 1]), scale2, negm2);
-          float p0, p1;
-          exp2_pair(x2, p0, p1);
-          ls2[c % 4] = add_x2(ls2[c % 4], f32x2(p0, p1));
-          pk[c] = pack_bf16x2(p0, p1);
-        }
+          for (int c = 0; c < kBN / 2; ++c) {
+            const uint64_t s2 = f32x2(s[2 * c], s[2 * c + 1]);
+            uint64_t u2 = scale2;
+            if constexpr (f.value != kCapTanh) u2 = cap_factor<f.value>(s2, args.mod.cap);
+            const uint64_t x2 = fma_x2(s2, u2, negm2);
+            float p0, p1;
+            exp2_pair(x2, p0, p1);
+            ls2[c % 4] = add_x2(ls2[c % 4], f32x2(p0, p1));
+            pk[c] = pack_bf16x2(p0, p1);
+          }
+        });
         float ls[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) f32x2_split(ls2[k], ls[2 * k], ls[2 * k + 1]);

@@ -144,7 +144,7 @@ struct RotaryArgs {
   int interleaved;
   int copy_rest;  // out is another buffer: elements from R on are copied
   float mscale, sign;
-  int tokens, heads_per_block;  // set by the launch
+  int tokens, heads_per_block, lanes;  // set by the launch
 };
 cudaError_t launch_rotary(const RotaryArgs& a, int elem_bytes, int num_sms, cudaStream_t stream);
 
@@ -163,7 +163,7 @@ struct TreeArgs {
   int piece_rows;  // workspace rows of one piece
   int page, num_pages, max_pages;
   int max_len;     // max_pages * page
-  float scale_log2, cap_y, cap_log2;
+  float scale, scale_log2, softcap;
   // workspace: [pieces][piece_rows][d] outputs, [pieces][piece_rows] (max, sum), [B + 1]
   float* parts;
   float2* stats;

@@ -19,6 +19,7 @@
 #pragma once
 
 #include <cstddef>
+#include <type_traits>
 
 #include "internal.h"
 #include "sm100.cuh"
@@ -31,6 +32,44 @@ constexpr int kModCap = 2;   // the same, and scores capped by a tanh
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// The tanh cap.  A raw product s becomes tanh's argument y = s * in; the capped score in
+// log2 units is out * tanh(y) = s q(s^2) with q the polynomial of a tile's range (below).
+struct CapArgs {
+  float in;             // scale / cap
+  float out;            // cap log2(e)
+  float inv_out2;       // 1 / out^2
+  float top3, top5;     // |s| up to which q3 and q5 hold (0: never)
+  float q3[4], q5[6];   // coefficients of (s^2)^i
+};
+
+// tanh(sqrt(u)) / sqrt(u) as polynomials in u, minimax in the relative error (fitted here
+// by iteratively reweighted least squares): 5.5e-7 for |y| <= 1/2, 5.9e-7 for |y| <= 1.
+inline CapArgs cap_args(float scale, float softcap) {
+  const double p3[4] = {0.9999994557706547, -0.33326317933916044, 0.13190296581699465,
+                        -0.04440222555557586};
+  const double p5[6] = {0.9999994135982464, -0.3332904237357338, 0.13281433841588497,
+                        -0.05160567291576986, 0.01674311383038407, -0.0030670598357108976};
+  CapArgs c{};
+  if (softcap <= 0.f) return c;
+  const double in = static_cast<double>(scale) / softcap;
+  const double out = 1.4426950408889634 * softcap;
+  c.in = static_cast<float>(in);
+  c.out = static_cast<float>(out);
+  c.inv_out2 = static_cast<float>(1.0 / (out * out));
+  // (a cap so far below the scale that the scaled coefficients could overflow leaves no
+  // score below it to speak of)
+  if (in < 100.0) {
+    c.top3 = static_cast<float>(0.5 / in);
+    c.top5 = static_cast<float>(1.0 / in);
+  }
+  double f = out * in;
+  for (int i = 0; i < 6; ++i, f *= in * in) {
+    if (i < 4) c.q3[i] = static_cast<float>(p3[i] * f);
+    c.q5[i] = static_cast<float>(p5[i] * f);
+  }
+  return c;
+}
+
 struct ModArgs {
   const int* doc_start;  // [B][Nk], or null
   const int* doc_end;
@@ -38,8 +77,7 @@ struct ModArgs {
   const float* slopes;   // [H], or null
   int Hkv;               // key heads
   int group;             // query heads of one key head
-  float cap_y;           // scale / cap: a raw product s becomes tanh's argument s * cap_y
-  float cap_log2;        // cap log2(e)
+  CapArgs cap;
 };
 
 inline ModArgs mod_args(const Problem& p) {
@@ -50,10 +88,7 @@ inline ModArgs mod_args(const Problem& p) {
   m.slopes = p.slopes;
   m.Hkv = p.Hkv;
   m.group = p.Hkv > 0 ? p.H / p.Hkv : 1;
-  if (p.softcap > 0.f) {
-    m.cap_y = p.scale / p.softcap;
-    m.cap_log2 = static_cast<float>(1.4426950408889634 * p.softcap);
-  }
+  m.cap = cap_args(p.scale, p.softcap);
   return m;
 }
 
@@ -101,60 +136,81 @@ __device__ __forceinline__ RowLimits mod_key(const ModArgs& m, int b, int j, int
   return r;
 }
 
-// tanh of N raw products times cap_y, in place (a thread's part of a score tile).
-//
-// Where every |y| of the warp is at most 1, tanh(y) = y P(y^2) with the degree-5 minimax
-// polynomial of tanh(sqrt(u)) / sqrt(u) on [0, 1] (fitted here by iteratively reweighted
-// least squares; relative error 6.7e-7 with the float32 evaluation): 4 packed
-// multiply-adds an entry and nothing on the exponential unit, which the probabilities
-// already fill.  Otherwise tanh(y) = 1 - 2 / (1 + e^{2y}), two more exponential-unit
-// operations an entry; its error is absolute, one float32 rounding at 1, which next to an
-// entry with |y| > 1 is below the rounding of that score, and it saturates to +-1 by
-// itself.  Scores of trained models lie well inside their cap, so the first form is the
-// usual one.
-constexpr float kTanh0 = 0x1.ffffecp-1f, kTanh1 = -0x1.554a16p-2f, kTanh2 = 0x1.1000f6p-3f,
-                kTanh3 = -0x1.a6c0f0p-5f, kTanh4 = 0x1.1251b4p-6f, kTanh5 = -0x1.92016ep-9f;
+// How a tile's capped scores are formed, from the largest |s| of the warp's entries:
+// kCap3, kCap5: x = s q(s^2), 1 + degree packed multiply-adds an entry (the last product
+// merges with the subtraction of the maximum) and nothing on the exponential unit, which
+// the probabilities fill already; kCapTanh: tanh(y) = 1 - 2 / (1 + e^{2y}), two more
+// exponential-unit operations an entry.  The error of the last is absolute, one float32
+// rounding at 1, which next to an entry with |y| > 1 is below that score's own rounding,
+// and it saturates to +-1 by itself.  Scores of trained models lie well inside their cap:
+// the polynomials are the usual case.
+constexpr int kCapTanh = 0, kCap3 = 3, kCap5 = 5;
 
 template <int N>
-__device__ __forceinline__ void tanh_scores(float* s, const ModArgs& m) {
-  using namespace sm100;
+__device__ __forceinline__ float abs_max(const float* s) {
   float a8[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) a8[k] = fabsf(s[k]);
 #pragma unroll
   for (int c = 8; c < N; c += 2)
-    a8[(c / 2) % 8] = max3(a8[(c / 2) % 8], fabsf(s[c]), fabsf(s[c + 1]));
-  const float amax = max3(max3(a8[0], a8[1], a8[2]), max3(a8[3], a8[4], a8[5]),
-                          fmaxf(a8[6], a8[7]));
-  if (!__any_sync(0xffffffffu, amax * m.cap_y > 1.f)) {
-    const uint64_t k2 = f32x2(m.cap_y, m.cap_y);
-#pragma unroll
-    for (int c = 0; c < N; c += 2) {
-      const uint64_t y = mul_x2(f32x2(s[c], s[c + 1]), k2);
-      const uint64_t u = mul_x2(y, y);
-      uint64_t q = fma_x2(u, f32x2(kTanh5, kTanh5), f32x2(kTanh4, kTanh4));
-      q = fma_x2(u, q, f32x2(kTanh3, kTanh3));
-      q = fma_x2(u, q, f32x2(kTanh2, kTanh2));
-      q = fma_x2(u, q, f32x2(kTanh1, kTanh1));
-      q = fma_x2(u, q, f32x2(kTanh0, kTanh0));
-      f32x2_split(mul_x2(y, q), s[c], s[c + 1]);
-    }
+    a8[(c / 2) % 8] = sm100::max3(a8[(c / 2) % 8], fabsf(s[c]), fabsf(s[c + 1]));
+  return sm100::max3(sm100::max3(a8[0], a8[1], a8[2]), sm100::max3(a8[3], a8[4], a8[5]),
+                     fmaxf(a8[6], a8[7]));
+}
+
+__device__ __forceinline__ int cap_form(float amax, const CapArgs& c) {
+  const bool over3 = !(amax <= c.top3), over5 = !(amax <= c.top5);
+  if (!__any_sync(0xffffffffu, over3)) return kCap3;
+  return __any_sync(0xffffffffu, over5) ? kCapTanh : kCap5;
+}
+
+// q(s^2) of a pair (kForm kCap3 or kCap5): the factor that takes s to log2 units.
+template <int kForm>
+__device__ __forceinline__ uint64_t cap_factor(uint64_t s2, const CapArgs& c) {
+  using namespace sm100;
+  const uint64_t u = mul_x2(s2, s2);
+  if constexpr (kForm == kCap3) {
+    uint64_t q = fma_x2(u, f32x2(c.q3[3], c.q3[3]), f32x2(c.q3[2], c.q3[2]));
+    q = fma_x2(u, q, f32x2(c.q3[1], c.q3[1]));
+    return fma_x2(u, q, f32x2(c.q3[0], c.q3[0]));
   } else {
-    const float k = 2.f * kLog2e * m.cap_y;
-#pragma unroll
-    for (int c = 0; c < N; ++c)
-      s[c] = fmaf(-2.f, rcp_approx(1.f + ex2_approx(s[c] * k)), 1.f);
+    uint64_t q = fma_x2(u, f32x2(c.q5[5], c.q5[5]), f32x2(c.q5[4], c.q5[4]));
+    q = fma_x2(u, q, f32x2(c.q5[3], c.q5[3]));
+    q = fma_x2(u, q, f32x2(c.q5[2], c.q5[2]));
+    q = fma_x2(u, q, f32x2(c.q5[1], c.q5[1]));
+    return fma_x2(u, q, f32x2(c.q5[0], c.q5[0]));
   }
 }
 
-// Two neighbouring entries of a score row or column in the backward pass: the
-// probabilities e = 2^(x - L2) and, with a cap, its derivatives g = 1 - tanh^2.  s0 and s1
-// are the raw products, or their tanh_scores with a cap; `unit2` turns them into log2
-// units.  nl holds -L2 of the two entries, the distance bias is sl * (pos_d + k) for entry
-// k, or sl * |pos_d + k| where the tile's keys lie on both sides of the position.
-template <int kMode>
+__device__ __forceinline__ float cap_tanh(float s, const CapArgs& c) {
+  const float e = sm100::ex2_approx(s * (2.f * kLog2e * c.in));
+  return fmaf(-2.f, sm100::rcp_approx(1.f + e), 1.f);
+}
+
+// N raw products to capped scores in log2 units, in place.
+template <int N>
+__device__ __forceinline__ void cap_scores(float* s, const CapArgs& c) {
+  using namespace sm100;
+  if (cap_form(abs_max<N>(s), c) != kCapTanh) {
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+      const uint64_t s2 = f32x2(s[k], s[k + 1]);
+      f32x2_split(mul_x2(s2, cap_factor<kCap5>(s2, c)), s[k], s[k + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] = c.out * cap_tanh(s[k], c);
+  }
+}
+
+// Two neighbouring entries of a score row or column in the backward pass, from their raw
+// products: the probabilities e = 2^(x - L2) and, with a cap, its derivatives
+// g = 1 - tanh^2 = 1 - (x / out)^2.  nl holds -L2 of the two entries, the distance bias is
+// sl * (pos_d + k) for entry k, or sl * |pos_d + k| where the tile's keys lie on both sides
+// of the position.
+template <int kMode, int kForm>
 __device__ __forceinline__ void mod_prob_pair(float s0, float s1, const ModArgs& m,
-                                              uint64_t unit2, uint64_t nl, float sl, float pos_d,
+                                              uint64_t scale2, uint64_t nl, float sl, float pos_d,
                                               bool straddles, float& e0, float& e1, float& g0,
                                               float& g1) {
   using namespace sm100;
@@ -167,11 +223,33 @@ __device__ __forceinline__ void mod_prob_pair(float s0, float s1, const ModArgs&
     nl = f32x2(n0, n1);
   }
   const uint64_t s2 = f32x2(s0, s1);
-  exp2_pair(fma_x2(s2, unit2, nl), e0, e1);
-  g0 = g1 = 1.f;
   if constexpr (kMode == kModCap) {
-    g0 = fmaf(-s0, s0, 1.f);
-    g1 = fmaf(-s1, s1, 1.f);
+    uint64_t x;
+    if constexpr (kForm == kCapTanh)
+      x = f32x2(m.cap.out * cap_tanh(s0, m.cap), m.cap.out * cap_tanh(s1, m.cap));
+    else
+      x = mul_x2(s2, cap_factor<kForm>(s2, m.cap));
+    exp2_pair(add_x2(x, nl), e0, e1);
+    const uint64_t g = fma_x2(mul_x2(x, x), f32x2(-m.cap.inv_out2, -m.cap.inv_out2), f32x2(1.f, 1.f));
+    f32x2_split(g, g0, g1);
+  } else {
+    exp2_pair(fma_x2(s2, scale2, nl), e0, e1);
+    g0 = g1 = 1.f;
+  }
+}
+
+// Calls f with the form as a compile-time constant (kCapTanh, kCap3 or kCap5).
+template <int kMode, typename F>
+__device__ __forceinline__ void with_cap_form(int form, const F& f) {
+  if constexpr (kMode == kModCap) {
+    if (form == kCap3)
+      f(std::integral_constant<int, kCap3>{});
+    else if (form == kCap5)
+      f(std::integral_constant<int, kCap5>{});
+    else
+      f(std::integral_constant<int, kCapTanh>{});
+  } else {
+    f(std::integral_constant<int, kCapTanh>{});
   }
 }
 

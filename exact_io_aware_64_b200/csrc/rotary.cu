@@ -8,13 +8,15 @@
 // Bound: HBM, each element read and written once.  A float32 product position * inv_freq
 // is off by 2^-24 of the angle, 0.006 rad at 10^5 rad, so the angle is formed in float64,
 // reduced to a fraction of a turn there, and only the fraction goes to float32 (error of
-// the angle 4e-7 rad).  That costs a few float64 operations and one sincospi per (token,
-// pair), so it is done once per block for kTokens tokens, kept in shared memory, and used
-// by every head of Q and K that the block turns; heads are dealt to the grid's y extent
-// when there are too few tokens to fill the GPU.
+// the angle 1e-7 rad).  That costs a few float64 operations and one sincospi per (token,
+// pair), so it must not be repeated for every head.
 //
-// A thread turns 16 bytes of elements at a time (both halves: two 16-byte loads) where
-// R and every stride and pointer allow it, and one pair at a time otherwise.
+// Vector form (R, strides and pointers allow 16-byte pieces): a thread owns one piece of a
+// head row at one token, forms its 2 to 8 angles once, in registers, and turns that piece
+// of every head of Q and K, four heads' loads in flight at a time; neighbouring threads hold
+// neighbouring pieces, then neighbouring tokens.  With few tokens, threads (then blocks)
+// share a token's heads.  Scalar form (anything else): one pair at a time, the angles in
+// shared memory.
 #include <cmath>
 #include <cstdint>
 
@@ -26,30 +28,29 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxTokens = 16;  // tokens of one block
+constexpr int kUnroll = 4;      // heads whose loads a thread has in flight
 
-// cos and sin (times m) of every pair of `n` tokens from token t0 of the flat [B*N] list
-__device__ __forceinline__ void fill_angles(float2* cs, const RotaryArgs& a, long long t0, int n) {
-  const int half = a.R / 2;
-  for (int i = threadIdx.x; i < n * half; i += kThreads) {
-    const int t = i / half, k = i - t * half;
-    const long long tok = t0 + t;
-    const double pos = a.positions != nullptr ? static_cast<double>(a.positions[tok])
-                                              : static_cast<double>(a.first + tok % a.N);
-    const double turns = pos * (static_cast<double>(a.inv_freq[k]) * 0.15915494309189533577);
-    const float f = static_cast<float>(2.0 * (turns - rint(turns)));
-    float s, c;
-    sincospif(f, &s, &c);
-    cs[i] = make_float2(c * a.mscale, s * a.mscale * a.sign);
-  }
+// cos and sin (times m) of pair k at flat token tok.
+__device__ __forceinline__ float2 angle(const RotaryArgs& a, double pos, int k) {
+  const double turns = pos * (static_cast<double>(a.inv_freq[k]) * 0.15915494309189533577);
+  const float f = static_cast<float>(2.0 * (turns - rint(turns)));
+  float s, c;
+  sincospif(f, &s, &c);
+  return make_float2(c * a.mscale, s * a.mscale * a.sign);
+}
+
+__device__ __forceinline__ double position(const RotaryArgs& a, int tok) {
+  return a.positions != nullptr ? static_cast<double>(a.positions[tok])
+                                : static_cast<double>(a.first + tok % a.N);
 }
 
 template <typename T>
-struct Vec;  // 16 bytes of elements as floats
+struct Vec;  // 16 bytes of elements
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int n = 8;
-  __device__ static void load(const __nv_bfloat16* p, float* x) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
+  __device__ static void unpack(uint4 v, float* x) {
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -58,23 +59,24 @@ struct Vec<__nv_bfloat16> {
       x[2 * i + 1] = f.y;
     }
   }
-  __device__ static void store(__nv_bfloat16* p, const float* x) {
+  __device__ static uint4 pack(const float* x) {
     uint4 v;
     __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    *reinterpret_cast<uint4*>(p) = v;
+    return v;
   }
 };
 template <>
 struct Vec<float> {
   static constexpr int n = 4;
-  __device__ static void load(const float* p, float* x) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  __device__ static void unpack(uint4 v, float* x) {
+    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
   }
-  __device__ static void store(float* p, const float* x) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  __device__ static uint4 pack(const float* x) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                      __float_as_uint(x[3]));
   }
 };
 
@@ -90,28 +92,85 @@ __device__ __forceinline__ void turn(float x1, float x2, float2 w, float& y1, fl
   y2 = fmaf(x2, w.x, __fmul_rn(x1, w.y));
 }
 
-// Element offset of (token, head) in a tensor of the given strides.
-__device__ __forceinline__ long long row_at(const RotaryTensor& x, long long b, long long n,
-                                            int h, bool out) {
-  return out ? b * x.out_b + h * x.out_h + n * x.out_n : b * x.in_b + h * x.in_h + n * x.in_n;
+template <typename T, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) rotary_vector_kernel(const RotaryArgs a) {
+  constexpr int kV = Vec<T>::n;
+  constexpr int kAngles = kInterleaved ? kV / 2 : kV;
+  const int half = a.R / 2;
+  const int turned = kInterleaved ? a.R / kV : half / kV;  // pieces of a row: turned, copied
+  const int pieces = turned + (a.copy_rest ? (a.d - a.R) / kV : 0);
+  // thread = (head group, token, piece), all powers of two but the last group
+  const int q = threadIdx.x & (a.lanes - 1);
+  const int t = (threadIdx.x / a.lanes) & (a.tokens - 1);
+  const int group = threadIdx.x / (a.lanes * a.tokens);
+  const int groups = kThreads / (a.lanes * a.tokens);
+  const long long tok_ll = static_cast<long long>(blockIdx.x) * a.tokens + t;
+  if (q >= pieces || tok_ll >= a.total) return;
+  const int tok = static_cast<int>(tok_ll);
+  const bool turns = q < turned;
+  float2 w[kAngles];
+  if (turns) {
+    const double pos = position(a, tok);
+#pragma unroll
+    for (int k = 0; k < kAngles; ++k) w[k] = angle(a, pos, q * kAngles + k);
+  }
+  const int e1 = turns ? q * kV : a.R + (q - turned) * kV;
+  const long long b = tok / a.N, n = tok - b * a.N;
+  const int h0 = blockIdx.y * a.heads_per_block;
+  const int h1 = min(h0 + a.heads_per_block, a.x[0].heads + a.x[1].heads);
+  const int nq = a.x[0].heads;
+  const T* src0 = static_cast<const T*>(a.x[0].in) + (b * a.x[0].in_b + n * a.x[0].in_n + e1);
+  const T* src1 = static_cast<const T*>(a.x[1].in) + (b * a.x[1].in_b + n * a.x[1].in_n + e1);
+  T* dst0 = static_cast<T*>(a.x[0].out) + (b * a.x[0].out_b + n * a.x[0].out_n + e1);
+  T* dst1 = static_cast<T*>(a.x[1].out) + (b * a.x[1].out_b + n * a.x[1].out_n + e1);
+  for (int hb = h0 + group; hb < h1; hb += groups * kUnroll) {
+    uint4 r1[kUnroll], r2[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = hb + u * groups;
+      if (h >= h1) break;
+      const T* p = h < nq ? src0 + h * a.x[0].in_h : src1 + (h - nq) * a.x[1].in_h;
+      r1[u] = *reinterpret_cast<const uint4*>(p);
+      if (!kInterleaved && turns) r2[u] = *reinterpret_cast<const uint4*>(p + half);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = hb + u * groups;
+      if (h >= h1) break;
+      T* p = h < nq ? dst0 + h * a.x[0].out_h : dst1 + (h - nq) * a.x[1].out_h;
+      if (turns) {
+        float x1[kV];
+        Vec<T>::unpack(r1[u], x1);
+        if constexpr (kInterleaved) {
+#pragma unroll
+          for (int k = 0; k < kAngles; ++k)
+            turn(x1[2 * k], x1[2 * k + 1], w[k], x1[2 * k], x1[2 * k + 1]);
+        } else {
+          float x2[kV];
+          Vec<T>::unpack(r2[u], x2);
+#pragma unroll
+          for (int k = 0; k < kAngles; ++k) turn(x1[k], x2[k], w[k], x1[k], x2[k]);
+          *reinterpret_cast<uint4*>(p + half) = Vec<T>::pack(x2);
+        }
+        r1[u] = Vec<T>::pack(x1);
+      }
+      *reinterpret_cast<uint4*>(p) = r1[u];
+    }
+  }
 }
 
-template <typename T, bool kInterleaved, bool kVector>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
-  extern __shared__ float2 cs[];
+template <typename T, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) rotary_scalar_kernel(const RotaryArgs a) {
+  extern __shared__ float2 cs[];  // [tokens][R/2]
   const int half = a.R / 2;
   const long long t0 = static_cast<long long>(blockIdx.x) * a.tokens;
   const int n = static_cast<int>(min(static_cast<long long>(a.tokens), a.total - t0));
-  fill_angles(cs, a, t0, n);
+  for (int i = threadIdx.x; i < n * half; i += kThreads)
+    cs[i] = angle(a, position(a, static_cast<int>(t0) + i / half), i % half);
   __syncthreads();
-  const int heads = a.x[0].heads + a.x[1].heads;
   const int h0 = blockIdx.y * a.heads_per_block;
-  const int hn = min(a.heads_per_block, heads - h0);
-  // pieces of one row: the turned part, then the copied part
-  constexpr int kV = kVector ? Vec<T>::n : 1;
-  const int turned = kVector ? (kInterleaved ? a.R / kV : half / kV) : half;
-  const int copied = a.copy_rest ? (a.d - a.R) / kV : 0;
-  const int per_row = turned + copied;
+  const int hn = min(a.heads_per_block, a.x[0].heads + a.x[1].heads - h0);
+  const int per_row = half + (a.copy_rest ? a.d - a.R : 0);  // pairs, then copied elements
   const int work = n * hn * per_row;
   for (int i = threadIdx.x; i < work; i += kThreads) {
     const int row = i / per_row, q = i - row * per_row;
@@ -120,42 +179,18 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
     const int which = h >= a.x[0].heads;
     const RotaryTensor& x = a.x[which];
     if (which) h -= a.x[0].heads;
-    const long long tok = t0 + t, b = tok / a.N, nn = tok - b * a.N;
-    const T* src = static_cast<const T*>(x.in) + row_at(x, b, nn, h, false);
-    T* dst = static_cast<T*>(x.out) + row_at(x, b, nn, h, true);
-    const float2* ang = cs + t * half;
-    if (q >= turned) {
-      const int e = a.R + (q - turned) * kV;
-      if constexpr (kVector) {
-        *reinterpret_cast<uint4*>(dst + e) = *reinterpret_cast<const uint4*>(src + e);
-      } else {
-        dst[e] = src[e];
-      }
-    } else if constexpr (!kVector) {
+    const int tok = static_cast<int>(t0) + t;
+    const long long b = tok / a.N, nn = tok - b * a.N;
+    const T* src = static_cast<const T*>(x.in) + (b * x.in_b + h * x.in_h + nn * x.in_n);
+    T* dst = static_cast<T*>(x.out) + (b * x.out_b + h * x.out_h + nn * x.out_n);
+    if (q >= half) {
+      dst[a.R + q - half] = src[a.R + q - half];
+    } else {
       const int e1 = kInterleaved ? 2 * q : q, e2 = kInterleaved ? 2 * q + 1 : q + half;
-      const float x1 = to_f(src[e1]), x2 = to_f(src[e2]);
       float y1, y2;
-      turn(x1, x2, ang[q], y1, y2);
+      turn(to_f(src[e1]), to_f(src[e2]), cs[t * half + q], y1, y2);
       put(dst + e1, y1);
       put(dst + e2, y2);
-    } else if constexpr (kInterleaved) {
-      float v[kV];
-      Vec<T>::load(src + q * kV, v);
-#pragma unroll
-      for (int k = 0; k < kV; k += 2) {
-        turn(v[k], v[k + 1], ang[(q * kV + k) / 2], v[k], v[k + 1]);
-      }
-      Vec<T>::store(dst + q * kV, v);
-    } else {
-      float v1[kV], v2[kV];
-      Vec<T>::load(src + q * kV, v1);
-      Vec<T>::load(src + half + q * kV, v2);
-#pragma unroll
-      for (int k = 0; k < kV; ++k) {
-        turn(v1[k], v2[k], ang[q * kV + k], v1[k], v2[k]);
-      }
-      Vec<T>::store(dst + q * kV, v1);
-      Vec<T>::store(dst + half + q * kV, v2);
     }
   }
 }
@@ -164,29 +199,41 @@ template <typename T>
 cudaError_t launch_t(const RotaryArgs& args, bool vector, int num_sms, cudaStream_t stream) {
   RotaryArgs a = args;
   const int heads = a.x[0].heads + a.x[1].heads;
-  // tokens of a block: few enough that the grid fills the GPU (two blocks per SM), at
-  // most 16 (the angles then take at most 16 KB and one block's rows are still long runs)
-  int tokens = 16;
+  int tokens = kMaxTokens;
+  if (vector) {
+    constexpr int kV = Vec<T>::n;
+    const int pieces = (a.interleaved ? a.R / kV : a.R / 2 / kV) +
+                       (a.copy_rest ? (a.d - a.R) / kV : 0);
+    a.lanes = 1;  // at most 128: d <= 512 float32 elements
+    while (a.lanes < pieces) a.lanes *= 2;
+    while (tokens * a.lanes > kThreads) tokens /= 2;
+  }
+  // with few tokens a block takes fewer of them, so that more blocks share the work
   while (tokens > 1 && a.total / tokens < 4ll * num_sms) tokens /= 2;
   a.tokens = tokens;
   const long long bx = (a.total + tokens - 1) / tokens;
-  int split = 1;  // blocks that share a token's heads, when there are few tokens
-  while (split < heads && bx * split < 2ll * num_sms) ++split;
-  if (split > 65535) split = 65535;
+  // blocks that share a token's heads, while a block still has a head for each group
+  const int groups = vector ? kThreads / (a.lanes * tokens) : 1;
+  int split = 1;
+  while (split * groups < heads && bx * split < 2ll * num_sms) ++split;
   a.heads_per_block = (heads + split - 1) / split;
   split = (heads + a.heads_per_block - 1) / a.heads_per_block;
+  if (split > 65535) {
+    a.heads_per_block = (heads + 65534) / 65535;
+    split = (heads + a.heads_per_block - 1) / a.heads_per_block;
+  }
   const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>(split));
-  const size_t smem = static_cast<size_t>(tokens) * (a.R / 2) * sizeof(float2);
-  if (a.interleaved) {
-    if (vector)
-      rotary_kernel<T, true, true><<<grid, kThreads, smem, stream>>>(a);
+  if (vector) {
+    if (a.interleaved)
+      rotary_vector_kernel<T, true><<<grid, kThreads, 0, stream>>>(a);
     else
-      rotary_kernel<T, true, false><<<grid, kThreads, smem, stream>>>(a);
+      rotary_vector_kernel<T, false><<<grid, kThreads, 0, stream>>>(a);
   } else {
-    if (vector)
-      rotary_kernel<T, false, true><<<grid, kThreads, smem, stream>>>(a);
+    const size_t smem = static_cast<size_t>(tokens) * (a.R / 2) * sizeof(float2);  // <= 32 KB
+    if (a.interleaved)
+      rotary_scalar_kernel<T, true><<<grid, kThreads, smem, stream>>>(a);
     else
-      rotary_kernel<T, false, false><<<grid, kThreads, smem, stream>>>(a);
+      rotary_scalar_kernel<T, false><<<grid, kThreads, smem, stream>>>(a);
   }
   return cudaGetLastError();
 }

@@ -118,11 +118,15 @@ __device__ __forceinline__ uint32_t seen_word(unsigned long long bits, int d0) {
   return static_cast<uint32_t>(d0 >= 0 ? bits >> d0 : bits << -d0 | ((1ull << -d0) - 1ull));
 }
 
+struct KernelArgs : TreeArgs {
+  CapArgs cap;
+};
+
 template <int D, bool kCap>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_sm100_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
+                      const __grid_constant__ CUtensorMap tmV, const KernelArgs a) {
   using L = Layout<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -366,10 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tSrow = tS[t] + lane_off, tOrow = tO[t] + lane_off;
     int s_count = 0, o_count = 0;
     bool ok = true;
-    ModArgs cap{};
-    cap.cap_y = a.cap_y;
-    cap.cap_log2 = a.cap_log2;
-    const float unit = kCap ? a.cap_log2 : a.scale_log2;
+    constexpr int kMode = kCap ? kModCap : kModNone;
     for (int pos = begin; ok && pos < end;) {
       const Unit u = tree_unit(a, prefix, pos, end);
       const int n = u.j1 - u.j0;
@@ -417,9 +418,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < kBN; ++c) s[c] = __uint_as_float(sr[c]);
         }
         const int kv0 = (u.j0 + i) * kBN;
+        // log2-unit score of entry c: s[c] * unit, or s[c] q(s[c]^2) (cap, form not kCapTanh)
+        float unit = a.scale_log2;
+        int form = kCapTanh;
+        const bool tail = kv0 + kBN > u.ctx;
         // drafted tokens are seen by their bits; slots behind the sequence's end have none
         auto hide = [&](float value) {
-          if (kv0 + kBN <= u.ctx) return;
+          if (!tail) return;
 #pragma unroll
           for (int q = 0; q < kBN / 32; ++q) {
             const uint32_t w = seen_word(bits, kv0 + 32 * q - u.ctx);
@@ -429,8 +434,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         if constexpr (kCap) {
-          hide(0.f);  // (what lies behind the end does not choose the form of the tanh)
-          tanh_scores<kBN>(s, cap);
+          if (tail || (form = cap_form(abs_max<kBN>(s), a.cap)) == kCapTanh) {
+            hide(0.f);  // (what lies behind the end does not choose the form of the tanh)
+            cap_scores<kBN>(s, a.cap);
+            unit = 1.f;
+            form = kCapTanh;
+          }
         }
         hide(-INFINITY);
         float mx8[8];
@@ -440,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 8; c < kBN; c += 2) mx8[(c / 2) % 8] = max3(mx8[(c / 2) % 8], s[c], s[c + 1]);
         const float mx = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]),
                               fmaxf(mx8[6], mx8[7]));
-        const float m_tile = mx * unit;
+        const float m_tile = kCap && form != kCapTanh ? a.cap.out * cap_tanh(mx, a.cap) : mx * unit;
         float alpha = 1.f;
         bool rescale = false;
         if (m_tile > m + kRescaleThreshold || m == -INFINITY) {
@@ -468,13 +477,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t pk[kBN / 2];
         const uint64_t unit2 = f32x2(unit, unit), negm2 = f32x2(-mref, -mref);
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
+        with_cap_form<kMode>(form, [&](auto f) {
 #pragma unroll
-        for (int c = 0; c < kBN / 2; ++c) {
-          float p0, p1;
-          exp2_pair(fma_x2(f32x2(s[2 * c], s[2 * c + 1]), unit2, negm2), p0, p1);
-          ls2[c % 4] = add_x2(ls2[c % 4], f32x2(p0, p1));
-          pk[c] = pack_bf16x2(p0, p1);
-        }
+          for (int c = 0; c < kBN / 2; ++c) {
+            const uint64_t s2 = f32x2(s[2 * c], s[2 * c + 1]);
+            uint64_t u2 = unit2;
+            if constexpr (f.value != kCapTanh) u2 = cap_factor<f.value>(s2, a.cap);
+            float p0, p1;
+            exp2_pair(fma_x2(s2, u2, negm2), p0, p1);
+            ls2[c % 4] = add_x2(ls2[c % 4], f32x2(p0, p1));
+            pk[c] = pack_bf16x2(p0, p1);
+          }
+        });
         float ls[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) f32x2_split(ls2[k], ls[2 * k], ls[2 * k + 1]);
@@ -602,7 +616,10 @@ cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = ready_kernel(kernel, kRegsLaunch, Layout<D>::bytes(kTreeMaxBatch), ready);
   if (e != cudaSuccess) return e;
-  kernel<<<num_sms, kThreads, Layout<D>::bytes(a.B), stream>>>(tmQ, tmK, tmV, a);
+  KernelArgs ka;
+  static_cast<TreeArgs&>(ka) = a;
+  ka.cap = cap_args(a.scale, a.softcap);
+  kernel<<<num_sms, kThreads, Layout<D>::bytes(a.B), stream>>>(tmQ, tmK, tmV, ka);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const long long rows = static_cast<long long>(a.B) * a.Hkv * a.rows;
   tree_join_kernel<D><<<static_cast<unsigned>(rows), kJoinThreads, 0, stream>>>(
@@ -615,7 +632,7 @@ cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
 cudaError_t launch_tree_sm100(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                               const CUtensorMap& tmV, void* O, float* LSE, const TreeArgs& a,
                               int d, int num_sms, cudaStream_t stream) {
-  const bool cap = a.cap_log2 > 0.f;
+  const bool cap = a.softcap > 0.f;
   auto launch = [&](auto* k) { return k(tmQ, tmK, tmV, O, LSE, a, num_sms, stream); };
   if (d == 64) return cap ? launch(launch_t<64, true>) : launch(launch_t<64, false>);
   return cap ? launch(launch_t<128, true>) : launch(launch_t<128, false>);

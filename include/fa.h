@@ -325,7 +325,8 @@ FA_API fa_status fa_doc_ranges(const int* doc_ids, int* doc_start, int* doc_end,
  *                (of the same document); needs causal = 1; taken as min(prefix, Nk), and
  *                a negative one as 0
  *   doc_start, doc_end in : [B,Nk] int32 from fa_doc_ranges over the key tokens, or both NULL
- *   softcap >= 0 and finite; 0 is no cap; d, scale, causal as in fa_fwd_qk.
+ *   softcap: 0 (no cap), or between 1e-9 and 1e9 with scale / softcap between 1e-12 and
+ *                1e12; d, scale, causal as in fa_fwd_qk.
  * A row that sees no key gets O = 0 and LSE = -inf.  K and V must hold finite values in
  * every row, visible or not (a hidden key's probability is zero, and 0 times a NaN is a
  * NaN).  doc_start and doc_end arrays of other origin that do not rise along the sequence
