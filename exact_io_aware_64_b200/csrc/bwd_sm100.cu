@@ -59,6 +59,7 @@ using namespace sm100;
 constexpr int kTile = 128;        // rows per query / key tile
 constexpr int kGroups = 2;        // element-wise warpgroups, splitting a tile's columns
 constexpr int kCols = kTile / kGroups;
+constexpr int kHalf = kCols / 2;  // columns whose P^T is announced together
 constexpr int kEw = kGroups * 128;  // element-wise threads
 constexpr int kThreads = kEw + 128;  // + a control warpgroup: TMA warp, MMA warp, 2 idle
 constexpr int kWarpTMA = kEw / 32;
@@ -218,7 +219,13 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(
     if (part == 0) {
       const size_t row = static_cast<size_t>(bh) * Npad + r;
       Dout[row] = -acc;
-      L2out[row] = r < lq ? -LSE[lse_index(a, bh, tq0, r)] * kLog2e : -INFINITY;
+      // (a row that saw no key, LSE = -inf, counts as a padded one: P = 0)
+      float nl2 = -INFINITY;
+      if (r < lq) {
+        const float lse = LSE[lse_index(a, bh, tq0, r)];
+        if (lse != -INFINITY) nl2 = -lse * kLog2e;
+      }
+      L2out[row] = nl2;
     }
   }
 }
@@ -388,15 +395,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (args.causal && j * kTile > off) i0 = (j * kTile - off) / kTile;
     m = (lq + kTile - 1) / kTile - i0;
   };
-  // query tile t of the unit: tile i of query head bhq
-  auto q_tile = [&](int bh, int i0, int m, int t, int& bhq, int& i) {
-    bhq = bh;
-    i = i0 + t;
-    if constexpr (kMode != kModNone) {
-      const int per = m / args.mod.group;
-      const int g = t / per;
-      bhq = bh * args.mod.group + g;
-      i = i0 + t - g * per;
+  // the unit's query tiles in turn: tile i of query head bhq, from (first head, i0) on
+  auto first_head = [&](int bh) { return kMode != kModNone ? bh * args.mod.group : bh; };
+  auto next_tile = [&](int i0, int end, int& bhq, int& i) {
+    if (++i == end) {  // (only modified scores have another head)
+      i = i0;
+      ++bhq;
     }
   };
   auto qslot = [&](int s) -> uint32_t { return base + L::kQ0 + s * L::kTileBytes; };
@@ -427,9 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                           tma_y(bh, j * kTile), tma_z(bh, tk0, j * kTile));
       }
       ++kv_loads;
-      for (int t = 0; ok && t < m; ++t) {
-        int bhq, i;
-        q_tile(bh, i0, m, t, bhq, i);
+      const int i_end = i0 + (kMode != kModNone ? m / args.mod.group : m);
+      int bhq = first_head(bh), i = i0;
+      for (int t = 0; ok && t < m; ++t, next_tile(i0, i_end, bhq, i)) {
         ok = wait_warp(bar(L::kBarQEmpty + qs), qph ^ 1);
         if (!ok) break;
         mbar_arrive_expect_tx_elect(bar(L::kBarQFull + qs), L::kTileBytes);
@@ -623,9 +627,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         full_lo = mod_key(args.mod, b, last, off, lq, lk, args.causal).lo;
         full_hi = mod_key(args.mod, b, first, off, lq, lk, args.causal).hi;
       }
-      for (int t = 0; t < m; ++t) {
-        int bhq, i;
-        q_tile(bh, i0, m, t, bhq, i);
+      const int i_end = i0 + (kMode != kModNone ? m / args.mod.group : m);
+      int bhq = first_head(bh), i = i0;
+      for (int t = 0; t < m; ++t, next_tile(i0, i_end, bhq, i)) {
         // this tile's L2 and D rows sit in its dO slot
         const uint8_t* sb = smem + L::kDO0 + stage * L::kDOSlotBytes;
         const float* sL = reinterpret_cast<const float*>(sb + L::kSlotL) + col0;
@@ -646,74 +650,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int delta = (j - i) * kTile - off;
           const bool diag = args.causal && delta > -kTile;
           const uint64_t scale2 = f32x2(args.scale_log2, args.scale_log2);
-          bool masked = false, straddles = false;
-          int mlo = 0;
-          unsigned width = 0;
-          float sl = 0.f, pos_d = 0.f;  // bias of column c: sl * (pos_d + c)
-          if constexpr (kMode != kModNone) {
-            masked = i * kTile + col0 < full_lo || i * kTile + col0 + kCols > full_hi;
-            mlo = lim_row.lo - i * kTile - col0;
-            width = static_cast<unsigned>(lim_row.hi - lim_row.lo);
-            if (args.mod.slopes != nullptr) {
-              // -slope |p - y|, y this thread's key, p = i*128 + off + column
-              sl = -args.mod.slopes[bhq % args.H] * kLog2e;
-              const int p0 = i * kTile + col0 + off;  // position of the group's column 0
-              pos_d = static_cast<float>(p0 - (j * kTile + row));
-              const bool before = p0 >= j * kTile + kTile - 1;      // keys before queries
-              const bool after = p0 + kCols - 1 <= j * kTile;       // keys after queries
-              straddles = !before && !after;
-              if (after && !before) sl = -sl;
-            }
+          float sc[kCols];
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) sc[c] = __uint_as_float(r[c]);
+          bool partial = false, over[2] = {};
+          float neg_slope = 0.f, at = 0.f;
+          if constexpr (kMode != kModNone)
+            partial = i * kTile + col0 < full_lo || i * kTile + col0 + kCols > full_hi;
+          if constexpr (has_bias(kMode)) {
+            // -slope |p - y|, y this thread's key, p = i*128 + off + column
+            neg_slope = args.mod.slopes[bhq % args.H] * -kLog2e;
+            at = static_cast<float>(i * kTile + col0 + off - (j * kTile + row));
           }
           // the group's 64 columns in two halves of 32; each half's bf16 P^T is stored and
           // announced as soon as it is made
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t pk[kCols / 4];
-            int form = kCapTanh;
-            if constexpr (kMode == kModCap) {
-              float raw[kCols / 2];
+            const int c0 = hf * kHalf;
+            if constexpr (kMode == kModNone) {
 #pragma unroll
-              for (int c = 0; c < kCols / 2; ++c) raw[c] = __uint_as_float(r[hf * (kCols / 2) + c]);
-              form = cap_form(abs_max<kCols / 2>(raw), args.mod.cap);
-            }
-            with_cap_form<kMode>(form, [&](auto f) {
-#pragma unroll
-              for (int c = hf * (kCols / 2); c < (hf + 1) * (kCols / 2); c += 2) {
+              for (int c = c0; c < c0 + kHalf; c += 2) {
                 // x = S^T * scale * log2e - L2 for two query columns in one packed FMA
                 const uint64_t nl = *reinterpret_cast<const uint64_t*>(sL + c);
+                const uint64_t x2 =
+                    fma_x2(f32x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), scale2, nl);
                 float e0, e1;
-                if constexpr (kMode == kModNone) {
-                  const uint64_t x2 =
-                      fma_x2(f32x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), scale2, nl);
-                  exp2_pair(x2, e0, e1);
-                  if (diag && col0 + c < row + delta) e0 = 0.f;
-                  if (diag && col0 + c + 1 < row + delta) e1 = 0.f;
-                  p[c] = e0;
-                  p[c + 1] = e1;
-                } else {
-                  float g0, g1;
-                  mod_prob_pair<kMode, f.value>(__uint_as_float(r[c]), __uint_as_float(r[c + 1]),
-                                                args.mod, scale2, nl, sl,
-                                                pos_d + static_cast<float>(c), straddles, e0, e1,
-                                                g0, g1);
-                  if (masked && static_cast<unsigned>(c - mlo) >= width) e0 = 0.f;
-                  if (masked && static_cast<unsigned>(c + 1 - mlo) >= width) e1 = 0.f;
-                  pk[c / 2 - hf * (kCols / 4)] = pack_bf16x2(e0, e1);
-                  // dS carries the cap's derivative
-                  p[c] = kMode == kModCap ? e0 * g0 : e0;
-                  p[c + 1] = kMode == kModCap ? e1 * g1 : e1;
-                }
+                exp2_pair(x2, e0, e1);
+                if (diag && col0 + c < row + delta) e0 = 0.f;
+                if (diag && col0 + c + 1 < row + delta) e1 = 0.f;
+                p[c] = e0;
+                p[c + 1] = e1;
               }
-            });
+            } else {
+              const int q0 = i * kTile + col0 + c0;
+              over[hf] = mod_probs<kMode, kHalf, true>(
+                  sc + c0, p + c0, pk, ColumnStat{sL + c0}, args.mod, args.scale_log2, neg_slope,
+                  at + static_cast<float>(c0), partial, lim_row.lo - q0, lim_row.hi - q0);
+            }
             if constexpr (kMode == kModNone) {
 #pragma unroll
               for (int c = 0; c < kCols / 4; ++c)
-                pk[c] = pack_bf16x2(p[hf * (kCols / 2) + 2 * c], p[hf * (kCols / 2) + 2 * c + 1]);
+                pk[c] = pack_bf16x2(p[c0 + 2 * c], p[c0 + 2 * c + 1]);
             }
             tmem_st16(tS + lane_off + col0 + hf * (kCols / 4), pk);
             tmem_wait_st();
             warp_arrive(bar(hf == 0 ? L::kBarPReady : L::kBarPReadyB));
+          }
+          if constexpr (has_cap(kMode)) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+              mod_slopes<kHalf>(sc + hf * kHalf, p + hf * kHalf, over[hf], args.mod.cap);
           }
         }
         ok = wait_warp(bar(L::kBarDPFull), dp_cnt & 1);
@@ -1168,14 +1155,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // modified scores: this row's visible keys, the keys that every row of the tile sees
       RowLimits lim_row{0, 0};
       int full_lo = 0, full_hi = 0;
-      float slope2 = 0.f;
+      float neg_slope = 0.f;
       if constexpr (kMode != kModNone) {
         const int b = bh / args.H;
         const int first = i * kTile, last = min(first + kTile, lq) - 1;
         lim_row = mod_row(args.mod, b, min(q_row, last), off, lk, args.causal);
         full_lo = mod_row(args.mod, b, last, off, lk, args.causal).lo;
         full_hi = mod_row(args.mod, b, first, off, lk, args.causal).hi;
-        if (args.mod.slopes != nullptr) slope2 = args.mod.slopes[bh % args.H] * kLog2e;
+        if constexpr (has_bias(kMode)) neg_slope = args.mod.slopes[bh % args.H] * -kLog2e;
       }
       for (int j = jb; j < jb + m; ++j) {
         ok = wait_warp(bar(L::kBarSFull), s_cnt & 1);
@@ -1199,35 +1186,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t scale2 = f32x2(args.scale_log2, args.scale_log2);
           const uint64_t nl2 = f32x2(nl2row, nl2row);
           if constexpr (kMode != kModNone) {
-            const bool masked = kv0 < full_lo || kv0 + kCols > full_hi;
-            const int mlo = lim_row.lo - kv0;
-            const unsigned width = static_cast<unsigned>(lim_row.hi - lim_row.lo);
-            // -slope |p - j| = sl (pos_d + c) before the tile's straddling keys are seen to
-            const int pos0 = i * kTile + off;
-            const bool before = kv0 + kCols - 1 <= pos0, after = kv0 >= pos0 + kTile - 1;
-            const float sl = before ? slope2 : -slope2;
-            const float pos_d = static_cast<float>(kv0 - (q_row + off));
-            int form = kCapTanh;
-            if constexpr (kMode == kModCap) {
-              float raw[kCols];
+            // distance bias -slope |p - j|, p this row's position, j = kv0 + column
+            const float at = static_cast<float>(kv0 - (q_row + off));
+            float sc[kCols];
 #pragma unroll
-              for (int c = 0; c < kCols; ++c) raw[c] = __uint_as_float(r[c]);
-              form = cap_form(abs_max<kCols>(raw), args.mod.cap);
-            }
-            with_cap_form<kMode>(form, [&](auto f) {
-#pragma unroll
-              for (int c = 0; c < kCols; c += 2) {
-                float e0, e1, g0, g1;
-                mod_prob_pair<kMode, f.value>(__uint_as_float(r[c]), __uint_as_float(r[c + 1]),
-                                              args.mod, scale2, nl2, sl,
-                                              pos_d + static_cast<float>(c), !before && !after, e0,
-                                              e1, g0, g1);
-                if (masked && static_cast<unsigned>(c - mlo) >= width) e0 = 0.f;
-                if (masked && static_cast<unsigned>(c + 1 - mlo) >= width) e1 = 0.f;
-                p[c] = kMode == kModCap ? e0 * g0 : e0;
-                p[c + 1] = kMode == kModCap ? e1 * g1 : e1;
-              }
-            });
+            for (int c = 0; c < kCols; ++c) sc[c] = __uint_as_float(r[c]);
+            const bool over = mod_probs<kMode, kCols, false>(
+                sc, p, nullptr, RowStat{nl2}, args.mod, args.scale_log2, neg_slope, at,
+                kv0 < full_lo || kv0 + kCols > full_hi, lim_row.lo - kv0, lim_row.hi - kv0);
+            if constexpr (has_cap(kMode)) mod_slopes<kCols>(sc, p, over, args.mod.cap);
           } else {
 #pragma unroll
           for (int c = 0; c < kCols; c += 2) {
@@ -1381,14 +1348,18 @@ cudaError_t launch_bwd_sm100(const CUtensorMap& tmQ, const CUtensorMap& tmK,
     return kernels(tmQ, tmK, tmV, tmdO, tmL2, tmD, tmdK, tmdV, O, dO, LSE, dQ, dK, dV, workspace,
                    p, num_sms, stream);
   };
-  const int mode = mod_mode(p);
-  if (p.d == 64)
-    return mode == kModNone  ? launch(launch_d<64, kModNone>)
-           : mode == kModCap ? launch(launch_d<64, kModCap>)
-                             : launch(launch_d<64, kModMask>);
-  return mode == kModNone  ? launch(launch_d<128, kModNone>)
-         : mode == kModCap ? launch(launch_d<128, kModCap>)
-                           : launch(launch_d<128, kModMask>);
+  switch (mod_mode(p) * 256 + p.d) {
+    case kModNone * 256 + 64: return launch(launch_d<64, kModNone>);
+    case kModNone * 256 + 128: return launch(launch_d<128, kModNone>);
+    case kModMask * 256 + 64: return launch(launch_d<64, kModMask>);
+    case kModMask * 256 + 128: return launch(launch_d<128, kModMask>);
+    case kModBias * 256 + 64: return launch(launch_d<64, kModBias>);
+    case kModBias * 256 + 128: return launch(launch_d<128, kModBias>);
+    case kModCap * 256 + 64: return launch(launch_d<64, kModCap>);
+    case kModCap * 256 + 128: return launch(launch_d<128, kModCap>);
+    case kModCapBias * 256 + 64: return launch(launch_d<64, kModCapBias>);
+    default: return launch(launch_d<128, kModCapBias>);
+  }
 }
 
 }  // namespace fa

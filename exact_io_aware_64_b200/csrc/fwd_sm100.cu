@@ -568,19 +568,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       // modified scores: this row's visible keys, the keys that every row of the tile
-      // sees, the tile's positions and the head's slope (log2 units)
+      // sees, and the head's slope (log2 units, negated)
       RowLimits lim_row{0, 0};
-      int full_lo = 0, full_hi = 0, pos0 = 0, pos1 = 0;
-      float slope2 = 0.f;
+      int full_lo = 0, full_hi = 0;
+      float neg_slope = 0.f;
       if constexpr (kMode != kModNone) {
         const int b = ui.bh / args.H;
         const int first = qt * kBM, last = min(first + kBM, ui.lq) - 1;
         lim_row = mod_row(args.mod, b, min(q_row, last), ui.off, args.Nk, args.causal);
         full_lo = mod_row(args.mod, b, last, ui.off, args.Nk, args.causal).lo;
         full_hi = mod_row(args.mod, b, first, ui.off, args.Nk, args.causal).hi;
-        pos0 = first + ui.off;
-        pos1 = first + kBM - 1 + ui.off;
-        if (args.mod.slopes != nullptr) slope2 = args.mod.slopes[ui.h] * kLog2e;
+        if constexpr (has_bias(kMode)) neg_slope = args.mod.slopes[ui.h] * -kLog2e;
       }
       float m = -INFINITY;  // running max, log2 units (scaled logits * log2 e)
       float l = 0.f;
@@ -599,48 +597,51 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kBN; ++c) s[c] = __uint_as_float(sr[c]);
         const int kv0 = (ui.jb + j) * kBN;
-        // log2-unit score of entry c: s[c] * unit + shift
-        // (with a cap and form kCap3 or kCap5, s[c] q(s[c]^2) instead)
-        float unit = args.scale_log2, shift = 0.f;
-        int form = kCapTanh;
+        // log2-unit score of entry c: s[c] * unit, or (capped) s[c] q(s[c]^2)
+        float unit = args.scale_log2;
+        float amax = 0.f;
+        bool capped = false;
         if constexpr (kMode != kModNone) {
           const bool partial = kv0 < full_lo || kv0 + kBN > full_hi;
-          if constexpr (kMode == kModCap) {
-            if (partial || slope2 != 0.f || (form = cap_form(abs_max<kBN>(s), args.mod.cap)) == kCapTanh) {
-              cap_scores<kBN>(s, args.mod.cap);
+          if constexpr (has_cap(kMode)) {
+            amax = abs_max<kBN>(s);
+            const bool over = cap_over(amax, args.mod.cap);
+            capped = !has_bias(kMode) && !partial && !over;
+            if (!capped) {
+              if (seldom(over)) {
+                cap_scores_any<kBN>(s, args.mod.cap);
+              } else {
+#pragma unroll
+                for (int c = 0; c < kBN; c += 2) {
+                  const uint64_t s2 = f32x2(s[c], s[c + 1]);
+                  f32x2_split(mul_x2(s2, cap_factor(s2, args.mod.cap)), s[c], s[c + 1]);
+                }
+              }
               unit = 1.f;
-              form = kCapTanh;
             }
           }
-          if (slope2 != 0.f) {
-            // -slope |p - j|, p the row's position: linear in the key inside a tile that
-            // lies wholly before or after the query tile, and the row's constant part is
-            // then added after the maximum
-            const float p = static_cast<float>(q_row + ui.off);
-            if (kv0 + kBN - 1 <= pos0 || kv0 >= pos1) {
-              const float sl = kv0 >= pos1 ? -slope2 : slope2;
-              shift = sl * (static_cast<float>(kv0) - p);
-              const uint64_t u2 = f32x2(unit, unit), step = f32x2(2.f * sl, 2.f * sl);
-              uint64_t b2 = f32x2(0.f, sl);
+          if constexpr (has_bias(kMode)) {
+            // -slope |p - j|, p this row's position
+            const float at = static_cast<float>(kv0 - (q_row + ui.off));
+            const uint64_t u2 = f32x2(unit, unit), sl2 = f32x2(neg_slope, neg_slope),
+                           two2 = f32x2(2.f, 2.f);
+            uint64_t d2 = f32x2(at, at + 1.f);
 #pragma unroll
-              for (int c = 0; c < kBN; c += 2) {
-                f32x2_split(fma_x2(f32x2(s[c], s[c + 1]), u2, b2), s[c], s[c + 1]);
-                b2 = add_x2(b2, step);
-              }
-            } else {
-              const float d0 = static_cast<float>(kv0) - p;
-#pragma unroll
-              for (int c = 0; c < kBN; ++c)
-                s[c] = s[c] * unit - slope2 * fabsf(d0 + static_cast<float>(c));
+            for (int c = 0; c < kBN; c += 2) {
+              f32x2_split(fma_x2(sl2, abs_x2(d2), mul_x2(f32x2(s[c], s[c + 1]), u2)), s[c],
+                          s[c + 1]);
+              d2 = add_x2(d2, two2);
             }
             unit = 1.f;
           }
           if (partial) {
-            const int lo = lim_row.lo - kv0;
-            const unsigned width = static_cast<unsigned>(lim_row.hi - lim_row.lo);
 #pragma unroll
-            for (int c = 0; c < kBN; ++c)
-              if (static_cast<unsigned>(c - lo) >= width) s[c] = -INFINITY;
+            for (int q = 0; q < kBN / 32; ++q) {
+              const uint32_t w = range_word(lim_row.lo - kv0 - 32 * q, lim_row.hi - kv0 - 32 * q);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!((w >> c) & 1u)) s[32 * q + c] = -INFINITY;
+            }
           }
         }
         // a ragged last key tile, or (causal) a tile whose last key lies past the
@@ -656,16 +657,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // row max as 8 independent chains of 3-input max folded at the end (a single
         // chain of 128 dependent max operations would sit on the critical path)
-        float mx8[8];
+        float m_tile;
+        if (has_cap(kMode) && capped) {
+          // the cap rises, so no score of the row is above that of its largest |s|, which
+          // serves as the reference as well as the largest score would (see cap_args)
+          m_tile = args.mod.cap.out * cap_tanh(amax, args.mod.cap);
+        } else {
+          float mx8[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mx8[k] = s[k];
+          for (int k = 0; k < 8; ++k) mx8[k] = s[k];
 #pragma unroll
-        for (int c = 8; c < kBN; c += 2) mx8[(c / 2) % 8] = max3(mx8[(c / 2) % 8], s[c], s[c + 1]);
-        const float mx = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]),
-                              fmaxf(mx8[6], mx8[7]));
-        float m_tile = kMode == kModNone ? mx * args.scale_log2 : fmaf(mx, unit, shift);
-        // (the cap rises, so the largest product has the largest score)
-        if (kMode == kModCap && form != kCapTanh) m_tile = args.mod.cap.out * cap_tanh(mx, args.mod.cap);
+          for (int c = 8; c < kBN; c += 2)
+            mx8[(c / 2) % 8] = max3(mx8[(c / 2) % 8], s[c], s[c + 1]);
+          const float mx = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]),
+                                fmaxf(mx8[6], mx8[7]));
+          m_tile = mx * (kMode == kModNone ? args.scale_log2 : unit);
+        }
         float alpha = 1.f;
         bool rescale = false;
         if (m_tile > m + kRescaleThreshold || m == -INFINITY) {
@@ -701,23 +708,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         // packed float pairs (one instruction per two entries), the exponentials on MUFU
         uint32_t pk[kBN / 2];
         const float sc = kMode == kModNone ? args.scale_log2 : unit;
-        const float negm = kMode == kModNone ? -mref : shift - mref;
         const uint64_t scale2 = f32x2(sc, sc);
-        const uint64_t negm2 = f32x2(negm, negm);
+        const uint64_t negm2 = f32x2(-mref, -mref);
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
-        with_cap_form<kMode>(form, [&](auto f) {
+        if (has_cap(kMode) && !has_bias(kMode) && capped) {
 #pragma unroll
           for (int c = 0; c < kBN / 2; ++c) {
             const uint64_t s2 = f32x2(s[2 * c], s[2 * c + 1]);
-            uint64_t u2 = scale2;
-            if constexpr (f.value != kCapTanh) u2 = cap_factor<f.value>(s2, args.mod.cap);
-            const uint64_t x2 = fma_x2(s2, u2, negm2);
+            float p0, p1;
+            exp2_pair(fma_x2(s2, cap_factor(s2, args.mod.cap), negm2), p0, p1);
+            ls2[c % 4] = add_x2(ls2[c % 4], f32x2(p0, p1));
+            pk[c] = pack_bf16x2(p0, p1);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kBN / 2; ++c) {
+            const uint64_t x2 = fma_x2(f32x2(s[2 * c], s[2 * c + 1]), scale2, negm2);
             float p0, p1;
             exp2_pair(x2, p0, p1);
             ls2[c % 4] = add_x2(ls2[c % 4], f32x2(p0, p1));
             pk[c] = pack_bf16x2(p0, p1);
           }
-        });
+        }
         float ls[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) f32x2_split(ls2[k], ls[2 * k], ls[2 * k + 1]);
@@ -865,14 +877,18 @@ cudaError_t launch_fwd_sm100(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                              const CUtensorMap& tmV, const CUtensorMap& tmO, void* O, float* LSE,
                              const Problem& p, int num_sms, cudaStream_t stream) {
   auto launch = [&](auto* kernel) { return kernel(tmQ, tmK, tmV, tmO, O, LSE, p, num_sms, stream); };
-  const int mode = mod_mode(p);
-  if (p.d == 64)
-    return mode == kModNone  ? launch(launch_d<64, kModNone>)
-           : mode == kModCap ? launch(launch_d<64, kModCap>)
-                             : launch(launch_d<64, kModMask>);
-  return mode == kModNone  ? launch(launch_d<128, kModNone>)
-         : mode == kModCap ? launch(launch_d<128, kModCap>)
-                           : launch(launch_d<128, kModMask>);
+  switch (mod_mode(p) * 256 + p.d) {
+    case kModNone * 256 + 64: return launch(launch_d<64, kModNone>);
+    case kModNone * 256 + 128: return launch(launch_d<128, kModNone>);
+    case kModMask * 256 + 64: return launch(launch_d<64, kModMask>);
+    case kModMask * 256 + 128: return launch(launch_d<128, kModMask>);
+    case kModBias * 256 + 64: return launch(launch_d<64, kModBias>);
+    case kModBias * 256 + 128: return launch(launch_d<128, kModBias>);
+    case kModCap * 256 + 64: return launch(launch_d<64, kModCap>);
+    case kModCap * 256 + 128: return launch(launch_d<128, kModCap>);
+    case kModCapBias * 256 + 64: return launch(launch_d<64, kModCapBias>);
+    default: return launch(launch_d<128, kModCapBias>);
+  }
 }
 
 }  // namespace fa

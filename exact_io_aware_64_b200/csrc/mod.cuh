@@ -18,54 +18,69 @@
 // clamped to the sequence.)
 #pragma once
 
+#include <cmath>
 #include <cstddef>
-#include <type_traits>
 
 #include "internal.h"
 #include "sm100.cuh"
 
 namespace fa {
 
-constexpr int kModNone = 0;  // scale and causal mask only: the unmodified calls
-constexpr int kModMask = 1;  // masks and distance bias
-constexpr int kModCap = 2;   // the same, and scores capped by a tanh
+// A kernel is compiled for one combination.  The element-wise loops are straight code of
+// several KB with two warps to a scheduler, so a second variant inside the same kernel is
+// paid for in instruction fetch: with all of them in one kernel the capped dK/dV and dQ
+// kernels ran 48 % and 39 % longer (383 and 260 us against 258 and 186 us, B=1 H=16 N=4096
+// d=128).  What a tile seldom needs (masks, scores near the cap) is kept short and apart.
+constexpr int kModNone = 0;      // scale and causal mask only: the unmodified calls
+constexpr int kModMask = 1;      // masks and shared heads
+constexpr int kModBias = 3;      // and distance bias
+constexpr int kModCap = 5;       // masks, shared heads and capped scores
+constexpr int kModCapBias = 7;   // all
+constexpr bool has_bias(int mode) { return (mode & 2) != 0; }
+constexpr bool has_cap(int mode) { return (mode & 4) != 0; }
+
+__device__ __forceinline__ bool seldom(bool x) { return __builtin_expect(x, 0); }
 
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The tanh cap.  A raw product s becomes tanh's argument y = s * in; the capped score in
-// log2 units is out * tanh(y) = s q(s^2) with q the polynomial of a tile's range (below).
+// log2 units is x = out * tanh(y) = s q(s^2), q a polynomial, while |s| <= top.  Scores of
+// trained models lie well inside their cap, so that is the usual case, and it needs nothing
+// of the exponential unit, which the probabilities fill.
 struct CapArgs {
-  float in;             // scale / cap
-  float out;            // cap log2(e)
-  float inv_out2;       // 1 / out^2
-  float top3, top5;     // |s| up to which q3 and q5 hold (0: never)
-  float q3[4], q5[6];   // coefficients of (s^2)^i
+  float in;        // scale / cap
+  float out;       // cap log2(e)
+  float neg_inv_out2;  // -1 / out^2
+  float top;       // |s| up to which q and g hold
+  float q[4];      // x = s q(s^2)
+  float g[3];      // 1 - tanh^2 = g(s^2), for the backward pass
 };
 
-// tanh(sqrt(u)) / sqrt(u) as polynomials in u, minimax in the relative error (fitted here
-// by iteratively reweighted least squares): 5.5e-7 for |y| <= 1/2, 5.9e-7 for |y| <= 1.
+// |y| <= 1/2: tanh(sqrt(u)) / sqrt(u) to degree 3, relative error 5.9e-7 evaluated in
+// float32, and sech^2(sqrt(u)) to degree 2, 1.6e-4 (it multiplies dS, which is rounded to
+// bf16 next, 2^-8).  Minimax in the relative error, fitted here by iteratively reweighted
+// least squares.
 inline CapArgs cap_args(float scale, float softcap) {
-  const double p3[4] = {0.9999994557706547, -0.33326317933916044, 0.13190296581699465,
-                        -0.04440222555557586};
-  const double p5[6] = {0.9999994135982464, -0.3332904237357338, 0.13281433841588497,
-                        -0.05160567291576986, 0.01674311383038407, -0.0030670598357108976};
+  const double p[4] = {0.9999994557706547, -0.33326317933916044, 0.13190296581699465,
+                       -0.04440222555557586};
+  const double d[3] = {0.9998382199693817, -0.9886407641960892, 0.5423509665406153};
   CapArgs c{};
   if (softcap <= 0.f) return c;
   const double in = static_cast<double>(scale) / softcap;
   const double out = 1.4426950408889634 * softcap;
   c.in = static_cast<float>(in);
   c.out = static_cast<float>(out);
-  c.inv_out2 = static_cast<float>(1.0 / (out * out));
-  // (a cap so far below the scale that the scaled coefficients could overflow leaves no
-  // score below it to speak of)
-  if (in < 100.0) {
-    c.top3 = static_cast<float>(0.5 / in);
-    c.top5 = static_cast<float>(1.0 / in);
-  }
-  double f = out * in;
-  for (int i = 0; i < 6; ++i, f *= in * in) {
-    if (i < 4) c.q3[i] = static_cast<float>(p3[i] * f);
-    c.q5[i] = static_cast<float>(p5[i] * f);
+  c.neg_inv_out2 = static_cast<float>(-1.0 / (out * out));
+  // The forward takes the score of a row's largest |s| for its reference maximum; scores
+  // then lie within 2 * 50 of it, so the largest probability is at least 2^-100, far from
+  // float32's (and bf16's) smallest: out * tanh(y) <= 50 bounds y for caps above 75.
+  double y = 0.5;
+  if (out * std::tanh(y) > 50.0) y = std::atanh(50.0 / out);
+  c.top = static_cast<float>(y / in);
+  double f = 1.0;
+  for (int i = 0; i < 4; ++i, f *= in * in) {
+    c.q[i] = static_cast<float>(p[i] * f * out * in);
+    if (i < 3) c.g[i] = static_cast<float>(d[i] * f);
   }
   return c;
 }
@@ -74,7 +89,7 @@ struct ModArgs {
   const int* doc_start;  // [B][Nk], or null
   const int* doc_end;
   const int* prefix;     // [B], or null
-  const float* slopes;   // [H], or null
+  const float* slopes;   // [H] (kModBias, kModCapBias)
   int Hkv;               // key heads
   int group;             // query heads of one key head
   CapArgs cap;
@@ -93,7 +108,8 @@ inline ModArgs mod_args(const Problem& p) {
 }
 
 inline int mod_mode(const Problem& p) {
-  return p.Hkv == 0 ? kModNone : p.softcap > 0.f ? kModCap : kModMask;
+  if (p.Hkv == 0) return kModNone;
+  return kModMask | (p.slopes != nullptr ? 2 : 0) | (p.softcap > 0.f ? 4 : 0);
 }
 
 struct RowLimits {
@@ -136,16 +152,6 @@ __device__ __forceinline__ RowLimits mod_key(const ModArgs& m, int b, int j, int
   return r;
 }
 
-// How a tile's capped scores are formed, from the largest |s| of the warp's entries:
-// kCap3, kCap5: x = s q(s^2), 1 + degree packed multiply-adds an entry (the last product
-// merges with the subtraction of the maximum) and nothing on the exponential unit, which
-// the probabilities fill already; kCapTanh: tanh(y) = 1 - 2 / (1 + e^{2y}), two more
-// exponential-unit operations an entry.  The error of the last is absolute, one float32
-// rounding at 1, which next to an entry with |y| > 1 is below that score's own rounding,
-// and it saturates to +-1 by itself.  Scores of trained models lie well inside their cap:
-// the polynomials are the usual case.
-constexpr int kCapTanh = 0, kCap3 = 3, kCap5 = 5;
-
 template <int N>
 __device__ __forceinline__ float abs_max(const float* s) {
   float a8[8];
@@ -158,98 +164,136 @@ __device__ __forceinline__ float abs_max(const float* s) {
                      fmaxf(a8[6], a8[7]));
 }
 
-__device__ __forceinline__ int cap_form(float amax, const CapArgs& c) {
-  const bool over3 = !(amax <= c.top3), over5 = !(amax <= c.top5);
-  if (!__any_sync(0xffffffffu, over3)) return kCap3;
-  return __any_sync(0xffffffffu, over5) ? kCapTanh : kCap5;
+// Whether some |s| of the warp is past the polynomials' range (or not a number).
+__device__ __forceinline__ bool cap_over(float amax, const CapArgs& c) {
+  return __any_sync(0xffffffffu, !(amax <= c.top));
 }
 
-// q(s^2) of a pair (kForm kCap3 or kCap5): the factor that takes s to log2 units.
-template <int kForm>
+// q(s^2) of a pair: the factor that takes s to its capped score in log2 units.
 __device__ __forceinline__ uint64_t cap_factor(uint64_t s2, const CapArgs& c) {
   using namespace sm100;
   const uint64_t u = mul_x2(s2, s2);
-  if constexpr (kForm == kCap3) {
-    uint64_t q = fma_x2(u, f32x2(c.q3[3], c.q3[3]), f32x2(c.q3[2], c.q3[2]));
-    q = fma_x2(u, q, f32x2(c.q3[1], c.q3[1]));
-    return fma_x2(u, q, f32x2(c.q3[0], c.q3[0]));
-  } else {
-    uint64_t q = fma_x2(u, f32x2(c.q5[5], c.q5[5]), f32x2(c.q5[4], c.q5[4]));
-    q = fma_x2(u, q, f32x2(c.q5[3], c.q5[3]));
-    q = fma_x2(u, q, f32x2(c.q5[2], c.q5[2]));
-    q = fma_x2(u, q, f32x2(c.q5[1], c.q5[1]));
-    return fma_x2(u, q, f32x2(c.q5[0], c.q5[0]));
-  }
+  uint64_t q = fma_x2(u, f32x2(c.q[3], c.q[3]), f32x2(c.q[2], c.q[2]));
+  q = fma_x2(u, q, f32x2(c.q[1], c.q[1]));
+  return fma_x2(u, q, f32x2(c.q[0], c.q[0]));
 }
 
+// tanh(s in) = 1 - 2 / (1 + e^{2y}): saturates to +-1 by itself; the error is absolute, one
+// float32 rounding at 1.
 __device__ __forceinline__ float cap_tanh(float s, const CapArgs& c) {
   const float e = sm100::ex2_approx(s * (2.f * kLog2e * c.in));
   return fmaf(-2.f, sm100::rcp_approx(1.f + e), 1.f);
 }
 
-// N raw products to capped scores in log2 units, in place.
+// The capped score in log2 units of any raw product: the polynomial where it holds (its
+// error is relative), the formula beyond.
+__device__ __forceinline__ float cap_any(float s, const CapArgs& c) {
+  const float u = s * s;
+  const float q = fmaf(u, fmaf(u, fmaf(u, c.q[3], c.q[2]), c.q[1]), c.q[0]);
+  return fabsf(s) <= c.top ? s * q : c.out * cap_tanh(s, c);
+}
+
 template <int N>
-__device__ __forceinline__ void cap_scores(float* s, const CapArgs& c) {
-  using namespace sm100;
-  if (cap_form(abs_max<N>(s), c) != kCapTanh) {
+__device__ __forceinline__ void cap_scores_any(float* s, const CapArgs& c) {
 #pragma unroll
-    for (int k = 0; k < N; k += 2) {
-      const uint64_t s2 = f32x2(s[k], s[k + 1]);
-      f32x2_split(mul_x2(s2, cap_factor<kCap5>(s2, c)), s[k], s[k + 1]);
+  for (int k = 0; k < N; ++k) s[k] = cap_any(s[k], c);
+}
+
+// Columns lo .. hi - 1 of 32 as bits (lo, hi any integers).
+__device__ __forceinline__ uint32_t range_word(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 32);
+  return hi <= lo ? 0u : (~0u >> (32 - (hi - lo))) << lo;
+}
+
+__device__ __forceinline__ uint64_t abs_x2(uint64_t v) {
+  float a, b;
+  sm100::f32x2_split(v, a, b);
+  return sm100::f32x2(fabsf(a), fabsf(b));
+}
+
+struct ColumnStat {  // a statistic per column, in shared memory
+  const float* at;
+  __device__ __forceinline__ uint64_t operator()(int c) const {
+    return *reinterpret_cast<const uint64_t*>(at + c);
+  }
+};
+struct RowStat {  // the same for every column
+  uint64_t pair;
+  __device__ __forceinline__ uint64_t operator()(int) const { return pair; }
+};
+
+// The backward pass's probabilities of N neighbouring entries of a score row or column,
+// p = 2^(x - L2) of the raw products s, 0 outside columns [lo, hi) (when `partial`), and
+// with kPack the bf16 pairs in pk.  nl(c) gives -L2 of columns c and c + 1 (-inf for a row
+// that sees nothing).  The distance bias of column c is neg_slope * |at + c|.  Returns
+// whether s now holds capped scores (some were past the polynomials' range).
+template <int kMode, int N, bool kPack, typename NL>
+__device__ __forceinline__ bool mod_probs(float* s, float* p, uint32_t* pk, const NL& nl,
+                                          const ModArgs& m, float scale_log2, float neg_slope,
+                                          float at, bool partial, int lo, int hi) {
+  using namespace sm100;
+  bool over = false;
+  float q0 = 0.f, q1 = 0.f, q2 = 0.f, q3 = 0.f;
+  if constexpr (has_cap(kMode)) {
+    q0 = m.cap.q[0], q1 = m.cap.q[1], q2 = m.cap.q[2], q3 = m.cap.q[3];
+    over = cap_over(abs_max<N>(s), m.cap);
+    if (seldom(over)) {
+      cap_scores_any<N>(s, m.cap);
+      q0 = 1.f, q1 = q2 = q3 = 0.f;
     }
-  } else {
+  }
+  const uint64_t scale2 = f32x2(scale_log2, scale_log2), two2 = f32x2(2.f, 2.f);
+  const uint64_t slope2 = f32x2(neg_slope, neg_slope);
+  uint64_t d2 = f32x2(at, at + 1.f);
 #pragma unroll
-    for (int k = 0; k < N; ++k) s[k] = c.out * cap_tanh(s[k], c);
+  for (int c = 0; c < N; c += 2) {
+    const uint64_t s2 = f32x2(s[c], s[c + 1]);
+    uint64_t n2 = nl(c);
+    if constexpr (has_bias(kMode)) {
+      n2 = fma_x2(slope2, abs_x2(d2), n2);
+      d2 = add_x2(d2, two2);
+    }
+    uint64_t f2 = scale2;
+    if constexpr (has_cap(kMode)) {
+      const uint64_t u = mul_x2(s2, s2);
+      f2 = fma_x2(u, f32x2(q3, q3), f32x2(q2, q2));
+      f2 = fma_x2(u, f2, f32x2(q1, q1));
+      f2 = fma_x2(u, f2, f32x2(q0, q0));
+    }
+    exp2_pair(fma_x2(s2, f2, n2), p[c], p[c + 1]);
+    if constexpr (kPack) pk[c / 2] = pack_bf16x2(p[c], p[c + 1]);
   }
+  if (seldom(partial)) {
+#pragma unroll
+    for (int q = 0; q < N / 32; ++q) {
+      const uint32_t w = range_word(lo - 32 * q, hi - 32 * q);
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        if (!((w >> c) & 1u)) p[32 * q + c] = 0.f;
+        if (!((w >> (c + 1)) & 1u)) p[32 * q + c + 1] = 0.f;
+        if constexpr (kPack) pk[16 * q + c / 2] = pack_bf16x2(p[32 * q + c], p[32 * q + c + 1]);
+      }
+    }
+  }
+  return over;
 }
 
-// Two neighbouring entries of a score row or column in the backward pass, from their raw
-// products: the probabilities e = 2^(x - L2) and, with a cap, its derivatives
-// g = 1 - tanh^2 = 1 - (x / out)^2.  nl holds -L2 of the two entries, the distance bias is
-// sl * (pos_d + k) for entry k, or sl * |pos_d + k| where the tile's keys lie on both sides
-// of the position.
-template <int kMode, int kForm>
-__device__ __forceinline__ void mod_prob_pair(float s0, float s1, const ModArgs& m,
-                                              uint64_t scale2, uint64_t nl, float sl, float pos_d,
-                                              bool straddles, float& e0, float& e1, float& g0,
-                                              float& g1) {
+// The cap's derivative into the probabilities that dS is made of: p[c] *= 1 - tanh^2, by
+// the polynomial of the raw products, or 1 - (x / out)^2 of capped scores (`over`).  Done
+// after the probabilities are handed to the MMA warp, while its products run.
+template <int N>
+__device__ __forceinline__ void mod_slopes(const float* s, float* p, bool over, const CapArgs& cap) {
   using namespace sm100;
-  if (m.slopes != nullptr) {
-    float n0, n1;
-    f32x2_split(nl, n0, n1);
-    const float d0 = pos_d, d1 = pos_d + 1.f;
-    n0 = fmaf(sl, straddles ? fabsf(d0) : d0, n0);
-    n1 = fmaf(sl, straddles ? fabsf(d1) : d1, n1);
-    nl = f32x2(n0, n1);
-  }
-  const uint64_t s2 = f32x2(s0, s1);
-  if constexpr (kMode == kModCap) {
-    uint64_t x;
-    if constexpr (kForm == kCapTanh)
-      x = f32x2(m.cap.out * cap_tanh(s0, m.cap), m.cap.out * cap_tanh(s1, m.cap));
-    else
-      x = mul_x2(s2, cap_factor<kForm>(s2, m.cap));
-    exp2_pair(add_x2(x, nl), e0, e1);
-    const uint64_t g = fma_x2(mul_x2(x, x), f32x2(-m.cap.inv_out2, -m.cap.inv_out2), f32x2(1.f, 1.f));
-    f32x2_split(g, g0, g1);
-  } else {
-    exp2_pair(fma_x2(s2, scale2, nl), e0, e1);
-    g0 = g1 = 1.f;
-  }
-}
-
-// Calls f with the form as a compile-time constant (kCapTanh, kCap3 or kCap5).
-template <int kMode, typename F>
-__device__ __forceinline__ void with_cap_form(int form, const F& f) {
-  if constexpr (kMode == kModCap) {
-    if (form == kCap3)
-      f(std::integral_constant<int, kCap3>{});
-    else if (form == kCap5)
-      f(std::integral_constant<int, kCap5>{});
-    else
-      f(std::integral_constant<int, kCapTanh>{});
-  } else {
-    f(std::integral_constant<int, kCapTanh>{});
+  const float g0 = over ? 1.f : cap.g[0], g1 = over ? cap.neg_inv_out2 : cap.g[1],
+              g2 = over ? 0.f : cap.g[2];
+#pragma unroll
+  for (int c = 0; c < N; c += 2) {
+    const uint64_t s2 = f32x2(s[c], s[c + 1]);
+    const uint64_t u = mul_x2(s2, s2);
+    uint64_t g = fma_x2(u, f32x2(g2, g2), f32x2(g1, g1));
+    g = fma_x2(u, g, f32x2(g0, g0));
+    f32x2_split(mul_x2(f32x2(p[c], p[c + 1]), g), p[c], p[c + 1]);
   }
 }
 

@@ -370,7 +370,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tSrow = tS[t] + lane_off, tOrow = tO[t] + lane_off;
     int s_count = 0, o_count = 0;
     bool ok = true;
-    constexpr int kMode = kCap ? kModCap : kModNone;
     for (int pos = begin; ok && pos < end;) {
       const Unit u = tree_unit(a, prefix, pos, end);
       const int n = u.j1 - u.j0;
@@ -418,9 +417,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < kBN; ++c) s[c] = __uint_as_float(sr[c]);
         }
         const int kv0 = (u.j0 + i) * kBN;
-        // log2-unit score of entry c: s[c] * unit, or s[c] q(s[c]^2) (cap, form not kCapTanh)
-        float unit = a.scale_log2;
-        int form = kCapTanh;
+        // log2-unit score of entry c: s[c] * unit, or (capped) s[c] q(s[c]^2)
+        float unit = a.scale_log2, amax = 0.f;
+        bool capped = false;
         const bool tail = kv0 + kBN > u.ctx;
         // drafted tokens are seen by their bits; slots behind the sequence's end have none
         auto hide = [&](float value) {
@@ -434,22 +433,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         if constexpr (kCap) {
-          if (tail || (form = cap_form(abs_max<kBN>(s), a.cap)) == kCapTanh) {
-            hide(0.f);  // (what lies behind the end does not choose the form of the tanh)
-            cap_scores<kBN>(s, a.cap);
+          amax = abs_max<kBN>(s);
+          capped = !tail && !cap_over(amax, a.cap);
+          if (!capped) {
+            cap_scores_any<kBN>(s, a.cap);
             unit = 1.f;
-            form = kCapTanh;
           }
         }
         hide(-INFINITY);
-        float mx8[8];
+        float m_tile;
+        if (kCap && capped) {  // (the score of the largest |s| is a reference as good: cap_args)
+          m_tile = a.cap.out * cap_tanh(amax, a.cap);
+        } else {
+          float mx8[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mx8[k] = s[k];
+          for (int k = 0; k < 8; ++k) mx8[k] = s[k];
 #pragma unroll
-        for (int c = 8; c < kBN; c += 2) mx8[(c / 2) % 8] = max3(mx8[(c / 2) % 8], s[c], s[c + 1]);
-        const float mx = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]),
-                              fmaxf(mx8[6], mx8[7]));
-        const float m_tile = kCap && form != kCapTanh ? a.cap.out * cap_tanh(mx, a.cap) : mx * unit;
+          for (int c = 8; c < kBN; c += 2)
+            mx8[(c / 2) % 8] = max3(mx8[(c / 2) % 8], s[c], s[c + 1]);
+          m_tile = unit * max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]),
+                               fmaxf(mx8[6], mx8[7]));
+        }
         float alpha = 1.f;
         bool rescale = false;
         if (m_tile > m + kRescaleThreshold || m == -INFINITY) {
@@ -477,18 +481,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t pk[kBN / 2];
         const uint64_t unit2 = f32x2(unit, unit), negm2 = f32x2(-mref, -mref);
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
-        with_cap_form<kMode>(form, [&](auto f) {
+        if (kCap && capped) {
 #pragma unroll
           for (int c = 0; c < kBN / 2; ++c) {
             const uint64_t s2 = f32x2(s[2 * c], s[2 * c + 1]);
-            uint64_t u2 = unit2;
-            if constexpr (f.value != kCapTanh) u2 = cap_factor<f.value>(s2, a.cap);
             float p0, p1;
-            exp2_pair(fma_x2(s2, u2, negm2), p0, p1);
+            exp2_pair(fma_x2(s2, cap_factor(s2, a.cap), negm2), p0, p1);
             ls2[c % 4] = add_x2(ls2[c % 4], f32x2(p0, p1));
             pk[c] = pack_bf16x2(p0, p1);
           }
-        });
+        } else {
+#pragma unroll
+          for (int c = 0; c < kBN / 2; ++c) {
+            float p0, p1;
+            exp2_pair(fma_x2(f32x2(s[2 * c], s[2 * c + 1]), unit2, negm2), p0, p1);
+            ls2[c % 4] = add_x2(ls2[c % 4], f32x2(p0, p1));
+            pk[c] = pack_bf16x2(p0, p1);
+          }
+        }
         float ls[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) f32x2_split(ls2[k], ls[2 * k], ls[2 * k + 1]);
