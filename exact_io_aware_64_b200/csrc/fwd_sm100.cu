@@ -611,11 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (seldom(over)) {
                 cap_scores_any<kBN>(s, args.mod.cap);
               } else {
-#pragma unroll
-                for (int c = 0; c < kBN; c += 2) {
-                  const uint64_t s2 = f32x2(s[c], s[c + 1]);
-                  f32x2_split(mul_x2(s2, cap_factor(s2, args.mod.cap)), s[c], s[c + 1]);
-                }
+                cap_scores<kBN>(s, args.mod.cap);
               }
               unit = 1.f;
             }

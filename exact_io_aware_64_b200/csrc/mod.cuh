@@ -193,10 +193,28 @@ __device__ __forceinline__ float cap_any(float s, const CapArgs& c) {
   return fabsf(s) <= c.top ? s * q : c.out * cap_tanh(s, c);
 }
 
+// N raw products to capped scores in place, by cap_any: for the tiles with a score past the
+// polynomial's range.  A rolled loop over a copy in local memory, so that what seldom runs
+// takes little of the instruction cache.
 template <int N>
 __device__ __forceinline__ void cap_scores_any(float* s, const CapArgs& c) {
+  float t[N];
 #pragma unroll
-  for (int k = 0; k < N; ++k) s[k] = cap_any(s[k], c);
+  for (int k = 0; k < N; ++k) t[k] = s[k];
+#pragma unroll 1
+  for (int k = 0; k < N; ++k) t[k] = cap_any(t[k], c);
+#pragma unroll
+  for (int k = 0; k < N; ++k) s[k] = t[k];
+}
+
+// The same by the polynomial.
+template <int N>
+__device__ __forceinline__ void cap_scores(float* s, const CapArgs& c) {
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    const uint64_t s2 = sm100::f32x2(s[k], s[k + 1]);
+    sm100::f32x2_split(sm100::mul_x2(s2, cap_factor(s2, c)), s[k], s[k + 1]);
+  }
 }
 
 // Columns lo .. hi - 1 of 32 as bits (lo, hi any integers).

@@ -433,10 +433,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         if constexpr (kCap) {
+          hide(0.f);  // (what lies behind the end does not choose the form)
           amax = abs_max<kBN>(s);
-          capped = !tail && !cap_over(amax, a.cap);
+          const bool over = cap_over(amax, a.cap);
+          capped = !tail && !over;
           if (!capped) {
-            cap_scores_any<kBN>(s, a.cap);
+            if (seldom(over))
+              cap_scores_any<kBN>(s, a.cap);
+            else
+              cap_scores<kBN>(s, a.cap);
             unit = 1.f;
           }
         }
