@@ -296,9 +296,28 @@ struct DkdvLayout {
   static constexpr int kBarPReadyB = kBarSFull + 7;  // second half of each group's P^T
   static constexpr int kNumBars = kBarPReadyB + 1;
   static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kAlloc = kMisc + 16;
+  static constexpr int kOrder = kMisc + 16;  // [kMaxOrdered] bytes: units by cost
+  static constexpr int kAlloc = kOrder + kMaxOrdered;
   static_assert(kAlloc <= 232448, "shared memory over the 227 KB per-block limit");
 };
+
+// Modified scores: the query tiles i0 .. i0 + n - 1 of each head that key tile j meets, and
+// the key tiles jb .. jb + n - 1 that query tile i meets (the limits rise from row to row).
+struct TileSpan {
+  int first, n;
+};
+__device__ __forceinline__ TileSpan key_tile_span(const BwdArgs& a, int b, int j) {
+  const int off = a.Nk - a.Nq, last = min(j * kTile + kTile, a.Nk) - 1;
+  const int lo = mod_key(a.mod, b, j * kTile, off, a.Nq, a.Nk, a.causal).lo;
+  const int hi = mod_key(a.mod, b, last, off, a.Nq, a.Nk, a.causal).hi;
+  return {lo / kTile, hi > lo ? (hi + kTile - 1) / kTile - lo / kTile : 0};
+}
+__device__ __forceinline__ TileSpan query_tile_span(const BwdArgs& a, int b, int i) {
+  const int off = a.Nk - a.Nq, last = min(i * kTile + kTile, a.Nq) - 1;
+  const int lo = mod_row(a.mod, b, i * kTile, off, a.Nk, a.causal).lo;
+  const int hi = mod_row(a.mod, b, last, off, a.Nk, a.causal).hi;
+  return {lo / kTile, hi > lo ? (hi + kTile - 1) / kTile - lo / kTile : 0};
+}
 
 template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -352,6 +371,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(L::kBarDrain), 1);
     fence_mbar_init();
   }
+  uint8_t* order = smem + L::kOrder;
+  if (kMode != kModNone && args.mod.ordered)
+    order_units(args.BH / args.mod.Hkv * args.n_kt, kThreads, reinterpret_cast<uint16_t*>(smem),
+                order, [&](int e) {
+                  const int b = e / args.n_kt;
+                  return key_tile_span(args, b, e - b * args.n_kt).n;
+                });
   if (warp == kWarpMMA) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
@@ -368,7 +394,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // group tiles each; the products of all of them add up in the same accumulators.
   auto unit = [&](int w, int& bh, int& j, int& i0, int& m, int& lk, int& off, int& tq0,
                   int& tk0, int& lq) {
-    if (args.causal) {
+    if (kMode != kModNone && args.mod.ordered) {
+      const int e = order[w / args.mod.Hkv];
+      const int b = e / args.n_kt;
+      j = e - b * args.n_kt;
+      bh = b * args.mod.Hkv + w % args.mod.Hkv;
+    } else if (args.causal) {
       j = w / args.BH;  // key tile 0 meets every query tile: heaviest first
       bh = w % args.BH;
     } else {
@@ -379,12 +410,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     off = lk - lq;  // position of query row 0 among the keys
     i0 = 0;
     if constexpr (kMode != kModNone) {
-      const int b = bh / args.mod.Hkv;
-      const int last = min(j * kTile + kTile, lk) - 1;
-      const int q_lo = mod_key(args.mod, b, j * kTile, off, lq, lk, args.causal).lo;
-      const int q_hi = mod_key(args.mod, b, last, off, lq, lk, args.causal).hi;
-      i0 = q_lo / kTile;
-      m = q_hi > q_lo ? ((q_hi + kTile - 1) / kTile - i0) * args.mod.group : 0;
+      const TileSpan span = key_tile_span(args, bh / args.mod.Hkv, j);
+      i0 = span.first;
+      m = span.n * args.mod.group;
       return;
     }
     if (j * kTile >= lk || lq == 0) {
@@ -833,7 +861,8 @@ struct DqLayout {
   static constexpr int kBarQTmem = kBarSFull + 7;   // this unit's Q, dO are in TMEM
   static constexpr int kNumBars = kBarQTmem + 1;
   static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kAlloc = kMisc + 16 + 1024;
+  static constexpr int kOrder = kMisc + 16;  // [kMaxOrdered] bytes: units by cost
+  static constexpr int kAlloc = kOrder + kMaxOrdered + 1024;
   static_assert(kAlloc <= 232448, "shared memory over the 227 KB per-block limit");
 };
 
@@ -887,6 +916,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(L::kBarQTmem), kEw / 32);
     fence_mbar_init();
   }
+  uint8_t* order = smem + L::kOrder;
+  if (kMode != kModNone && args.mod.ordered)
+    order_units(args.BH / args.H * args.n_qt, kThreads, reinterpret_cast<uint16_t*>(smem), order,
+                [&](int e) {
+                  const int b = e / args.n_qt;
+                  return query_tile_span(args, b, e - b * args.n_qt).n;
+                });
   if (warp == kWarpMMA) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
@@ -913,7 +949,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto unit = [&](int w, int& bh, int& i, int& jb, int& m, int& lq, int& lk, int& off, int& tq0,
                   int& tk0) {
     jb = 0;
-    if (args.causal) {
+    if (kMode != kModNone && args.mod.ordered) {
+      const int e = order[w / args.H];
+      const int b = e / args.n_qt;
+      i = e - b * args.n_qt;
+      bh = b * args.H + w % args.H;
+    } else if (args.causal) {
       i = args.n_qt - 1 - w / args.BH;  // last query tile meets the most key tiles
       bh = w % args.BH;
     } else {
@@ -923,12 +964,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     seq_info(args, bh, lq, lk, tq0, tk0);
     off = lk - lq;
     if constexpr (kMode != kModNone) {
-      const int b = bh / args.H;
-      const int last = min(i * kTile + kTile, lq) - 1;
-      const int lo = mod_row(args.mod, b, i * kTile, off, lk, args.causal).lo;
-      const int hi = mod_row(args.mod, b, last, off, lk, args.causal).hi;
-      jb = lo / kTile;
-      m = hi > lo ? (hi + kTile - 1) / kTile - jb : 0;
+      const TileSpan span = query_tile_span(args, bh / args.H, i);
+      jb = span.first;
+      m = span.n;
       return;
     }
     if (i * kTile >= lq || lk == 0) {
@@ -1317,6 +1355,9 @@ cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   if constexpr (kMode != kModNone) a_kv.BH = p.BH / a.mod.group;  // heads of K and V
   a_kv.total_units = a_kv.BH * a.n_kt;
   a_q.total_units = p.BH * a.n_qt;
+  const bool docs = p.doc_start != nullptr;
+  a_kv.mod.ordered = docs && p.BH / p.H * a.n_kt <= kMaxOrdered;
+  a_q.mod.ordered = docs && p.BH / p.H * a.n_qt <= kMaxOrdered;
   const int grid_kv = a_kv.total_units < num_sms ? a_kv.total_units : num_sms;
   const int grid_q = a_q.total_units < num_sms ? a_q.total_units : num_sms;
   static std::atomic<uint64_t> ready_kv{0}, ready_q{0};

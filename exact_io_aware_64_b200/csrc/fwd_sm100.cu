@@ -113,7 +113,8 @@ struct FwdLayout {
   static constexpr int kBarSFree = 13 + 2 * kStages;  // [2] (separate-P layout only)
   static constexpr int kNumBars = 15 + 2 * kStages;
   static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kBytes = kMisc + 16;
+  static constexpr int kOrder = kMisc + 16;  // [kMaxOrdered] bytes: units by cost
+  static constexpr int kBytes = kOrder + kMaxOrdered;
   static constexpr int kAlloc = kBytes + 1024;  // room to align the base to 1024 bytes
 };
 
@@ -145,11 +146,43 @@ struct UnitInfo {
   int h, tq0, tk0;    // head; packed layout: the sequence's first query and key token
 };
 
+// Modified scores: the key tiles that the unit's two row tiles walk.  Both start at the
+// unit's first visible tile; the limits rise from row to row, so a tile's first and last
+// rows bound it.
+struct UnitSpan {
+  int jb, n0, n1;
+};
+__device__ __forceinline__ UnitSpan unit_span(const FwdArgs& a, int b, int u) {
+  const int off = a.Nk - a.Nq;
+  int e[2];
+  UnitSpan r;
+  r.jb = a.Nk;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int r0 = (2 * u + t) * kBM;
+    e[t] = 0;
+    if (r0 >= a.Nq) continue;
+    const int lo = mod_row(a.mod, b, r0, off, a.Nk, a.causal).lo;
+    const int hi = mod_row(a.mod, b, min(r0 + kBM, a.Nq) - 1, off, a.Nk, a.causal).hi;
+    if (hi <= lo) continue;  // no row of the tile sees a key
+    r.jb = min(r.jb, lo / kBN);
+    e[t] = (hi + kBN - 1) / kBN;
+  }
+  r.n0 = max(e[0] - r.jb, 0);
+  r.n1 = max(e[1] - r.jb, 0);
+  return r;
+}
+
 template <int kMode>
-__device__ __forceinline__ UnitInfo unit_info(int w, const FwdArgs& a) {
+__device__ __forceinline__ UnitInfo unit_info(int w, const FwdArgs& a, const uint8_t* order) {
   UnitInfo r;
   r.jb = 0;
-  if (a.causal) {
+  if (kMode != kModNone && a.mod.ordered) {
+    const int e = order[w / a.H];
+    const int b = e / a.n_units;
+    r.u = e - b * a.n_units;
+    r.bh = b * a.H + w % a.H;
+  } else if (a.causal) {
     // heaviest units (largest query index) first, all heads of one row-band together
     r.u = a.n_units - 1 - w / a.BH;
     r.bh = w % a.BH;
@@ -164,26 +197,13 @@ __device__ __forceinline__ UnitInfo unit_info(int w, const FwdArgs& a) {
   r.tk0 = 0;
   r.kbh = r.bh;
   if constexpr (kMode != kModNone) {
-    // both tiles walk the keys from the unit's first visible tile on; the limits rise
-    // from row to row, so a tile's first and last rows bound it
     const int b = r.bh / a.H;
     r.kbh = b * a.mod.Hkv + r.h / a.mod.group;
     r.off = r.lk - r.lq;
-    int e[2];
-    r.jb = a.Nk;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int r0 = (2 * r.u + t) * kBM;
-      e[t] = 0;
-      if (r0 >= r.lq) continue;
-      const int lo = mod_row(a.mod, b, r0, r.off, a.Nk, a.causal).lo;
-      const int hi = mod_row(a.mod, b, min(r0 + kBM, r.lq) - 1, r.off, a.Nk, a.causal).hi;
-      if (hi <= lo) continue;  // no row of the tile sees a key
-      r.jb = min(r.jb, lo / kBN);
-      e[t] = (hi + kBN - 1) / kBN;
-    }
-    r.n0 = max(e[0] - r.jb, 0);
-    r.n1 = max(e[1] - r.jb, 0);
+    const UnitSpan span = unit_span(a, b, r.u);
+    r.jb = span.jb;
+    r.n0 = span.n0;
+    r.n1 = span.n1;
     return r;
   }
   if (a.cu_q != nullptr) {
@@ -280,6 +300,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmV);
     tma_prefetch_desc(&tmO);
   }
+  uint8_t* order = smem + L::kOrder;
+  if (kMode != kModNone && args.mod.ordered) {
+    order_units(args.BH / args.H * args.n_units, kThreads, reinterpret_cast<uint16_t*>(smem), order,
+                [&](int e) {
+                  const int b = e / args.n_units;
+                  const UnitSpan span = unit_span(args, b, e - b * args.n_units);
+                  return max(span.n0, span.n1);
+                });
+  }
   if (warp == kWarpMMA) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
@@ -308,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t issued_phase[L::kStages];
       for (int s = 0; s < L::kStages; ++s) issued[s] = 0, issued_phase[s] = 0;
       for (int r = 0, w = snake_unit(0); ok && w < args.total_units; w = snake_unit(++r)) {
-        const UnitInfo ui = unit_info<kMode>(w, args);
+        const UnitInfo ui = unit_info<kMode>(w, args, order);
         if (ui.n0 == 0 && ui.n1 == 0) continue;  // no work in this unit (every role skips it)
         for (int t = 0; t < 2 && ok; ++t) {
           if ((t == 0 ? ui.n0 : ui.n1) == 0) continue;
@@ -411,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ring = 0;
         int s_tot[2] = {0, 0};
         for (int r = 0, w = snake_unit(0); ok && w < args.total_units; w = snake_unit(++r)) {
-          const UnitInfo ui = unit_info<kMode>(w, args);
+          const UnitInfo ui = unit_info<kMode>(w, args, order);
           if (ui.n0 == 0 && ui.n1 == 0) continue;  // no work in this unit
           const int nt[2] = {ui.n0, ui.n1};
           const int n = max(ui.n0, ui.n1);
@@ -485,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
       for (int r = 0, w = snake_unit(0); ok && w < args.total_units; w = snake_unit(++r)) {
-        const UnitInfo ui = unit_info<kMode>(w, args);
+        const UnitInfo ui = unit_info<kMode>(w, args, order);
         if (ui.n0 == 0 && ui.n1 == 0) continue;  // no work in this unit
         const int nt[2] = {ui.n0, ui.n1};
         const int n = max(ui.n0, ui.n1);
@@ -550,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool st_used = false;  // this warp's O staging box has been handed to a bulk store
     bool ok = true;
     for (int r = 0, w = snake_unit(0); ok && w < args.total_units; w = snake_unit(++r)) {
-      const UnitInfo ui = unit_info<kMode>(w, args);
+      const UnitInfo ui = unit_info<kMode>(w, args, order);
       const int n_t = t == 0 ? ui.n0 : ui.n1;
       const int qt = 2 * ui.u + t;
       const int q_row = qt * kBM + row;
@@ -857,6 +886,7 @@ cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   a.total_units = p.BH * a.n_units;
   a.scale_log2 = p.scale * kLog2e;
   a.mod = mod_args(p);
+  a.mod.ordered = p.doc_start != nullptr && p.BH / p.H * a.n_units <= kMaxOrdered;
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = ready_kernel(fwd_sm100_kernel<D, kMode>, kRegsLaunch, L::kAlloc, ready);
   if (e != cudaSuccess) return e;

@@ -92,6 +92,7 @@ struct ModArgs {
   const float* slopes;   // [H] (kModBias, kModCapBias)
   int Hkv;               // key heads
   int group;             // query heads of one key head
+  int ordered;           // the kernel ranks its units by cost (order_units)
   CapArgs cap;
 };
 
@@ -150,6 +151,31 @@ __device__ __forceinline__ RowLimits mod_key(const ModArgs& m, int b, int j, int
   r.lo = min(max(lo - off, 0), Nq);
   r.hi = max(min(hi - off, Nq), r.lo);
   return r;
+}
+
+// Work units of documents differ in cost by far more than causal ones, and not in order of
+// their index: the units (n of them, one head's) are ranked by cost(e), dearest first, for
+// the persistent kernels' dealing order.  Called by all `threads` threads of a CTA before
+// its pipelines start; `scratch` is n uint16 of shared memory that a TMA load may write
+// later, `order` n bytes that stay.  A __syncthreads() must follow.
+constexpr int kMaxOrdered = 256;
+
+template <typename Cost>
+__device__ __forceinline__ void order_units(int n, int threads, uint16_t* scratch, uint8_t* order,
+                                            const Cost& cost) {
+  for (int e = threadIdx.x; e < n; e += threads)
+    scratch[e] = static_cast<uint16_t>(min(cost(e), 65535));
+  __syncthreads();
+  for (int e = threadIdx.x; e < n; e += threads) {
+    const int c = scratch[e];
+    int rank = 0;
+    for (int k = 0; k < n; ++k) {
+      const int o = scratch[k];
+      rank += o > c || (o == c && k < e);
+    }
+    order[rank] = static_cast<uint8_t>(e);
+  }
+  sm100::fence_proxy_async_shared();
 }
 
 template <int N>
