@@ -120,28 +120,30 @@ def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:
     return s.cuda_stream
 
 
-def _run(name: str, device: torch.device, stream: Optional[torch.cuda.Stream], *args) -> None:
-    """Call ``name`` on ``stream`` (default: the current stream of ``device``) with
-    ``device`` current.  The host's part of a small call takes longer than its kernel, so
-    nothing is looked up twice: the raw handle of the current stream instead of a Stream
-    object (0.2 us against 7 us), and no device change where the device is current."""
+def _run(name: str, index: int, *args) -> None:
+    """Call ``name`` on the current stream of device ``index``, with that device current.
+    The host's part of a small call takes longer than its kernel, so nothing is looked up
+    twice: the raw handle of the current stream instead of a Stream object (0.2 us against
+    7 us), and no device change where the device is current."""
     fn = _fns.get(name)
     if fn is None:
         fn = _fns[name] = getattr(lib(), name)
-    index = device.index
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
-    elif stream.device_index != index:
-        raise ValueError(f"stream is on device {stream.device_index}, the tensors on {index}")
-    else:
-        handle = stream.cuda_stream
+    handle = torch._C._cuda_getCurrentRawStream(index)
     if torch.cuda.current_device() == index:
         st = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             st = fn(*args, handle)
     if st != FA_OK:
         _check(name, st)
+
+
+def _on(stream: torch.cuda.Stream, t: torch.Tensor):
+    """Context in which a call given ``stream`` runs: what it allocates (a workspace that is
+    freed on return among it) then belongs to that stream, and what it fills is filled there."""
+    if not t.is_cuda or stream.device_index != t.get_device():
+        raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -473,23 +475,32 @@ def bwd_packed(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tenso
     return dQ, dK, dV
 
 
-def _check_like(name: str, t: Optional[torch.Tensor], shape: tuple, dtype, device,
-                optional: bool = False) -> None:
-    """t is a contiguous tensor of this shape, dtype and device (or None when optional)."""
-    if t is None and optional:
-        return
-    if t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
+def _like(t: Optional[torch.Tensor], shape: tuple, dtype, index: int) -> bool:
+    """t is None, or a contiguous tensor of this shape and dtype on CUDA device ``index``."""
+    return t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == index
+                         and t.is_contiguous())
+
+
+def _check_like(name: str, t: torch.Tensor, shape: tuple, dtype, index: int) -> None:
+    if t is not None and _like(t, shape, dtype, index):
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on the inputs' device ({device}), not {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the inputs' device (cuda:{index}), not {t.device}")
     raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got "
                      f"{t.dtype} {tuple(t.shape)}")
 
 
-def _check_workspace(t: torch.Tensor, device) -> int:
-    if t.device != device or not t.is_contiguous():
+def _check_all(index: int, *wanted) -> None:
+    """Each of ``wanted`` is (name, tensor or None, shape, dtype)."""
+    for name, t, shape, dtype in wanted:
+        if not _like(t, shape, dtype, index):
+            _check_like(name, t, shape, dtype, index)
+
+
+def _check_workspace(t: torch.Tensor, index: int) -> int:
+    if t.get_device() != index or not t.is_contiguous():
         raise ValueError("workspace must be contiguous and on the inputs' device")
     return t.numel() * t.element_size()
 
@@ -501,36 +512,48 @@ def doc_ranges(doc_ids: torch.Tensor, starts: Optional[torch.Tensor] = None,
     ``fa_doc_ranges``: doc_ids [B, N] int32 (an id per key token, negative for padding)
     -> (starts, ends), [B, N] int32 each, the run of equal ids every token lies in.  One
     call serves every layer's forward and backward calls over the batch."""
+    if stream is not None:
+        with _on(stream, doc_ids):
+            return doc_ranges(doc_ids, starts, ends)
     if doc_ids.dim() != 2:
         raise ValueError("doc_ids must have two dimensions [B, N]")
-    B, N = doc_ids.shape
-    device = doc_ids.device
-    _check_bhnd("doc_ids", doc_ids, (B, N), torch.int32)
+    B, N = shape = doc_ids.shape
+    index = doc_ids.get_device()
+    _check_bhnd("doc_ids", doc_ids, shape, torch.int32)
+    _check_all(index, ("starts", starts, shape, torch.int32), ("ends", ends, shape, torch.int32))
     starts = torch.empty_like(doc_ids) if starts is None else starts
     ends = torch.empty_like(doc_ids) if ends is None else ends
-    _check_like("starts", starts, (B, N), torch.int32, device)
-    _check_like("ends", ends, (B, N), torch.int32, device)
-    _run("fa_doc_ranges", device, stream, _ptr(doc_ids), _ptr(starts), _ptr(ends), B, N)
+    _run("fa_doc_ranges", index, doc_ids.data_ptr(), starts.data_ptr(), ends.data_ptr(),
+         B, N)
     return starts, ends
 
 
-def _mod_shapes(Q, K, V, slopes, prefix, docs):
+def _mod_args(Q, K, V, slopes, prefix, docs, *more):
+    """Check a _mod call's inputs (``more``: further tensors as (name, tensor, True for Q's
+    shape or False for K's)); its sizes, device and the pointers of its modifications."""
     if Q.dim() != 4 or K.dim() != 4:
         raise ValueError("Q must be [B, H, Nq, d] and K, V [B, Hkv, Nk, d]")
-    B, H, Nq, d = Q.shape
+    B, H, Nq, d = q_shape = Q.shape
     Hkv, Nk = K.shape[1], K.shape[2]
-    device = Q.device
-    _check_bhnd("Q", Q, (B, H, Nq, d), torch.bfloat16)
-    _check_like("K", K, (B, Hkv, Nk, d), torch.bfloat16, device)
-    _check_like("V", V, (B, Hkv, Nk, d), torch.bfloat16, device)
-    _check_like("slopes", slopes, (H,), torch.float32, device, optional=True)
-    _check_like("prefix", prefix, (B,), torch.int32, device, optional=True)
+    k_shape = (B, Hkv, Nk, d)
+    bf16, index = torch.bfloat16, Q.get_device()
+    _check_bhnd("Q", Q, q_shape, bf16)
+    if not (_like(K, k_shape, bf16, index) and _like(V, k_shape, bf16, index)):
+        _check_like("K", K, k_shape, bf16, index)
+        _check_like("V", V, k_shape, bf16, index)
+    for name, t, like_q in more:
+        shape = q_shape if like_q else k_shape
+        if not _like(t, shape, bf16, index):
+            _check_like(name, t, shape, bf16, index)
     starts, ends = (None, None) if docs is None else docs
-    if docs is not None:
-        _check_like("docs[0]", starts, (B, Nk), torch.int32, device)
-        _check_like("docs[1]", ends, (B, Nk), torch.int32, device)
-    mods = (_ptr(slopes), _ptr(prefix), _ptr(starts), _ptr(ends))
-    return B, H, Hkv, Nq, Nk, d, device, mods
+    if docs is not None and (starts is None or ends is None):
+        raise ValueError("docs must be the pair that doc_ranges returns")
+    if slopes is not None or prefix is not None or docs is not None:
+        _check_all(index, ("slopes", slopes, (H,), torch.float32),
+                   ("prefix", prefix, (B,), torch.int32),
+                   ("docs[0]", starts, (B, Nk), torch.int32),
+                   ("docs[1]", ends, (B, Nk), torch.int32))
+    return B, H, Hkv, Nq, Nk, d, index, (_ptr(slopes), _ptr(prefix), _ptr(starts), _ptr(ends))
 
 
 def fwd_mod(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: Optional[float] = None,
@@ -547,19 +570,20 @@ def fwd_mod(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: Optional[f
     ``docs`` = ``doc_ranges(ids)`` hides keys of other documents.  A row that sees no key
     gets O = 0 and LSE = -inf.  Returns (O, LSE); LSE is None when ``want_lse`` is False
     and none is passed."""
-    B, H, Hkv, Nq, Nk, d, device, mods = _mod_shapes(Q, K, V, slopes, prefix, docs)
+    if stream is not None:
+        with _on(stream, Q):
+            return fwd_mod(Q, K, V, scale, causal, softcap, slopes, prefix, docs, O, LSE, want_lse)
+    B, H, Hkv, Nq, Nk, d, index, mods = _mod_args(Q, K, V, slopes, prefix, docs, ("O", O, True))
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if O is None:
         O = torch.empty_like(Q)
-    else:
-        _check_like("O", O, (B, H, Nq, d), torch.bfloat16, device)
     if LSE is not None:
-        _check_like("LSE", LSE, (B, H, Nq), torch.float32, device)
+        _check_like("LSE", LSE, (B, H, Nq), torch.float32, index)
     elif want_lse:
-        LSE = torch.empty((B, H, Nq), device=device, dtype=torch.float32)
-    _run("fa_fwd_mod", device, stream, _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(LSE), *mods, B,
-         H, Hkv, Nq, Nk, d, float(scale), int(bool(causal)), float(softcap))
+        LSE = Q.new_empty((B, H, Nq), dtype=torch.float32)
+    _run("fa_fwd_mod", index, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
+         _ptr(LSE), *mods, B, H, Hkv, Nq, Nk, d, scale, int(bool(causal)), softcap)
     return O, LSE
 
 
@@ -573,26 +597,25 @@ def bwd_mod(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tensor,
     """Backward of ``fwd_mod`` with the same modifications through ``fa_bwd_mod``.  dK and
     dV [B, Hkv, Nk, d] are summed over the query heads that share a key head; slopes are
     constants.  Every row of every gradient is written.  Returns (dQ, dK, dV)."""
-    B, H, Hkv, Nq, Nk, d, device, mods = _mod_shapes(Q, K, V, slopes, prefix, docs)
-    q_shape, k_shape = (B, H, Nq, d), (B, Hkv, Nk, d)
-    _check_like("O", O, q_shape, torch.bfloat16, device)
-    _check_like("dO", dO, q_shape, torch.bfloat16, device)
-    _check_like("LSE", LSE, (B, H, Nq), torch.float32, device)
+    if stream is not None:
+        with _on(stream, Q):
+            return bwd_mod(Q, K, V, O, dO, LSE, scale, causal, softcap, slopes, prefix, docs, dQ,
+                           dK, dV, workspace)
+    B, H, Hkv, Nq, Nk, d, index, mods = _mod_args(
+        Q, K, V, slopes, prefix, docs, ("O", O, True), ("dO", dO, True), ("dQ", dQ, True),
+        ("dK", dK, False), ("dV", dV, False))
+    _check_like("LSE", LSE, (B, H, Nq), torch.float32, index)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     dQ = torch.empty_like(Q) if dQ is None else dQ
     dK = torch.empty_like(K) if dK is None else dK
     dV = torch.empty_like(V) if dV is None else dV
-    _check_like("dQ", dQ, q_shape, torch.bfloat16, device)
-    _check_like("dK", dK, k_shape, torch.bfloat16, device)
-    _check_like("dV", dV, k_shape, torch.bfloat16, device)
     if workspace is None:
-        workspace = torch.empty(max(workspace_bytes(B, H, Nq, d), 16), device=device,
-                                dtype=torch.uint8)
-    ws_bytes = _check_workspace(workspace, device)
-    _run("fa_bwd_mod", device, stream, _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(dO), _ptr(LSE),
-         _ptr(dQ), _ptr(dK), _ptr(dV), *mods, B, H, Hkv, Nq, Nk, d, float(scale),
-         int(bool(causal)), float(softcap), _ptr(workspace), ws_bytes)
+        workspace = Q.new_empty(max(workspace_bytes(B, H, Nq, d), 16), dtype=torch.uint8)
+    ws_bytes = _check_workspace(workspace, index)
+    _run("fa_bwd_mod", index, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
+         dO.data_ptr(), LSE.data_ptr(), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), *mods, B, H,
+         Hkv, Nq, Nk, d, scale, int(bool(causal)), softcap, workspace.data_ptr(), ws_bytes)
     return dQ, dK, dV
 
 
@@ -632,48 +655,66 @@ def rotary_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0,
     return freq.float().to(device), mscale
 
 
-def _rotary_side(name, x, out, dtype, device):
-    """(B, heads, N, d) and the stride array of one tensor of a rotary call; None for the
-    strides of contiguous [B, heads, N, d] tensors."""
+def _rotary_strides(name, x, out, dtype, index):
+    """The stride array of one tensor of a rotary call; None for contiguous [B, heads, N, d]
+    tensors."""
     for what, t in ((name, x), (f"{name}'s output", out)):
-        if t.dtype != dtype or t.device != device or not t.is_cuda:
-            raise ValueError(f"{what} must be a {dtype} CUDA tensor on {device}, got {t.dtype} "
-                             f"on {t.device}")
+        if t.dtype is not dtype or t.get_device() != index:
+            raise ValueError(f"{what} must be a {dtype} CUDA tensor on the inputs' device, got "
+                             f"{t.dtype} on {t.device}")
         if t.dim() not in (3, 4) or t.shape != x.shape:
             raise ValueError(f"{what} must be [B, heads, N, d] or packed [tokens, heads, d]")
-    if x.dim() == 4 and x.is_contiguous() and out.is_contiguous():
-        return x.shape, None
-    for what, t in ((name, x), (f"{name}'s output", out)):
         if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
             raise ValueError(f"{what} must be contiguous in its last dimension")
+    i, o = x.stride(), out.stride()
     if x.dim() == 3:
-        N, heads, d = x.shape
-        st = [0, x.stride(1), x.stride(0), 0, out.stride(1), out.stride(0)]
-        return (1, heads, N, d), (_ll * 6)(*st)
-    return x.shape, (_ll * 6)(*x.stride()[:3], *out.stride()[:3])
+        return (_ll * 6)(0, i[1], i[0], 0, o[1], o[0])
+    return (_ll * 6)(*i[:3], *o[:3])
 
 
 def _rotary(Q, K, inv_freq, positions, first, interleaved, mscale, Q_out, K_out, inverse, stream):
-    dtype, device = Q.dtype, Q.device
-    if dtype not in (torch.bfloat16, torch.float32):
+    if stream is not None:
+        with _on(stream, Q):
+            return _rotary(Q, K, inv_freq, positions, first, interleaved, mscale, Q_out, K_out,
+                           inverse, None)
+    dtype, index = Q.dtype, Q.get_device()
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError("Q and K must be bfloat16 or float32")
+    if not Q.is_cuda:
+        raise ValueError("Q must be a CUDA tensor")
+    packed = Q.dim() == 3
+    if not packed and Q.dim() != 4:
+        raise ValueError("Q must be [B, heads, N, d] or packed [tokens, heads, d]")
     Q_out = torch.empty_like(Q) if Q_out is None else Q_out
-    (B, H, N, d), qs = _rotary_side("Q", Q, Q_out, dtype, device)
-    Hkv, ks = 0, None
+    q_shape = Q.shape
+    qs = ks = None
+    if packed or not (Q.is_contiguous() and _like(Q_out, q_shape, dtype, index)):
+        qs = _rotary_strides("Q", Q, Q_out, dtype, index)
+    if packed:
+        (N, H, d), B = q_shape, 1
+    else:
+        B, H, N, d = q_shape
+    Hkv = 0
     if K is not None:
-        K_out = torch.empty_like(K) if K_out is None else K_out
-        (Bk, Hkv, Nk, dk), ks = _rotary_side("K", K, K_out, dtype, device)
-        if (Bk, Nk, dk) != (B, N, d) or K.dim() != Q.dim():
+        k_shape = K.shape
+        Hkv = k_shape[1] if len(k_shape) > 1 else 0
+        if k_shape != ((N, Hkv, d) if packed else (B, Hkv, N, d)):
             raise ValueError("Q and K must agree in batch, tokens and head dimension")
+        K_out = torch.empty_like(K) if K_out is None else K_out
+        if packed or not (_like(K, k_shape, dtype, index) and _like(K_out, k_shape, dtype, index)):
+            ks = _rotary_strides("K", K, K_out, dtype, index)
     elif K_out is not None:
         raise ValueError("K_out without K")
-    R = 2 * inv_freq.numel()
-    _check_like("inv_freq", inv_freq, (R // 2,), torch.float32, device)
+    half = inv_freq.numel()
+    if not _like(inv_freq, (half,), torch.float32, index):
+        _check_like("inv_freq", inv_freq, (half,), torch.float32, index)
     if positions is not None:
-        _check_like("positions", positions, (N,) if Q.dim() == 3 else (B, N), torch.int32, device)
-    _run("fa_rotary" if dtype == torch.bfloat16 else "fa_rotary_f32", device, stream, _ptr(Q),
-         _ptr(Q_out), _ptr(K), _ptr(K_out), _ptr(inv_freq), _ptr(positions), int(first), B, H,
-         Hkv, N, d, R, int(bool(interleaved)), inverse, float(mscale), qs, ks)
+        shape = (N,) if packed else (B, N)
+        if not _like(positions, shape, torch.int32, index):
+            _check_like("positions", positions, shape, torch.int32, index)
+    _run("fa_rotary" if dtype is torch.bfloat16 else "fa_rotary_f32", index, Q.data_ptr(),
+         Q_out.data_ptr(), _ptr(K), _ptr(K_out), inv_freq.data_ptr(), _ptr(positions), first, B, H,
+         Hkv, N, d, 2 * half, int(bool(interleaved)), inverse, mscale, qs, ks)
     return Q_out, K_out
 
 
@@ -723,39 +764,49 @@ def fwd_tree(Q: torch.Tensor, K_cache: torch.Tensor, V_cache: torch.Tensor,
     Rows behind a sequence's drafted tokens are not written (outputs allocated here start
     as zeros and -inf when ``seqlens_q`` is given).  Returns (O, LSE); LSE is None when
     ``want_lse`` is False and none is passed."""
+    if stream is not None:
+        with _on(stream, Q):
+            return fwd_tree(Q, K_cache, V_cache, block_table, cache_lens, seqlens_q, tree_mask,
+                            scale, softcap, O, LSE, want_lse, workspace)
     if Q.dim() != 4 or K_cache.dim() != 4 or block_table.dim() != 2:
         raise ValueError("Q must be [B, H, T, d], the caches [num_pages, Hkv, page, d] and "
                          "block_table [B, max_pages]")
     B, H, T, d = Q.shape
     num_pages, Hkv, page, _ = K_cache.shape
     max_pages = block_table.shape[1]
-    device = Q.device
+    index, bf16, i32 = Q.get_device(), torch.bfloat16, torch.int32
     cache = (num_pages, Hkv, page, d)
-    _check_bhnd("Q", Q, (B, H, T, d), torch.bfloat16)
-    _check_like("K_cache", K_cache, cache, torch.bfloat16, device)
-    _check_like("V_cache", V_cache, cache, torch.bfloat16, device)
-    _check_like("block_table", block_table, (B, max_pages), torch.int32, device)
-    _check_like("cache_lens", cache_lens, (B,), torch.int32, device)
-    _check_like("seqlens_q", seqlens_q, (B,), torch.int32, device, optional=True)
-    _check_like("tree_mask", tree_mask, (B, T), torch.int64, device, optional=True)
+    _check_bhnd("Q", Q, (B, H, T, d), bf16)
+    if not (_like(K_cache, cache, bf16, index) and _like(V_cache, cache, bf16, index)
+            and _like(block_table, (B, max_pages), i32, index)
+            and _like(cache_lens, (B,), i32, index)):
+        _check_like("K_cache", K_cache, cache, bf16, index)
+        _check_like("V_cache", V_cache, cache, bf16, index)
+        _check_like("block_table", block_table, (B, max_pages), i32, index)
+        _check_like("cache_lens", cache_lens, (B,), i32, index)
+    if seqlens_q is not None:
+        _check_like("seqlens_q", seqlens_q, (B,), i32, index)
+    if tree_mask is not None:
+        _check_like("tree_mask", tree_mask, (B, T), torch.int64, index)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    if O is None:
-        O = torch.empty_like(Q) if seqlens_q is None else torch.zeros_like(Q)
+    if O is not None:
+        _check_like("O", O, (B, H, T, d), bf16, index)
     else:
-        _check_like("O", O, (B, H, T, d), torch.bfloat16, device)
+        O = torch.empty_like(Q) if seqlens_q is None else torch.zeros_like(Q)
     if LSE is not None:
-        _check_like("LSE", LSE, (B, H, T), torch.float32, device)
+        _check_like("LSE", LSE, (B, H, T), torch.float32, index)
     elif want_lse:
-        LSE = torch.empty((B, H, T), device=device, dtype=torch.float32) if seqlens_q is None \
-            else torch.full((B, H, T), float("-inf"), device=device)
+        LSE = Q.new_empty((B, H, T), dtype=torch.float32)
+        if seqlens_q is not None:
+            LSE.fill_(-math.inf)
     if workspace is None:
-        workspace = torch.empty(max(tree_workspace_bytes(B, H, Hkv, T, d), 16), device=device,
-                                dtype=torch.uint8)
-    ws_bytes = _check_workspace(workspace, device)
-    _run("fa_fwd_tree", device, stream, _ptr(Q), _ptr(K_cache), _ptr(V_cache), _ptr(O), _ptr(LSE),
-         _ptr(block_table), _ptr(cache_lens), _ptr(seqlens_q), _ptr(tree_mask), B, H, Hkv, T,
-         num_pages, page, max_pages, d, float(scale), float(softcap), _ptr(workspace), ws_bytes)
+        workspace = Q.new_empty(max(tree_workspace_bytes(B, H, Hkv, T, d), 16), dtype=torch.uint8)
+    ws_bytes = _check_workspace(workspace, index)
+    _run("fa_fwd_tree", index, Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(),
+         O.data_ptr(), _ptr(LSE), block_table.data_ptr(), cache_lens.data_ptr(), _ptr(seqlens_q),
+         _ptr(tree_mask), B, H, Hkv, T, num_pages, page, max_pages, d, scale, softcap,
+         workspace.data_ptr(), ws_bytes)
     return O, LSE
 
 
