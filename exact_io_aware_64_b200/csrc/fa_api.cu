@@ -637,7 +637,7 @@ TreeSplit tree_split(int B, int H, int Hkv, int T) {
   TreeSplit s;
   s.rows = static_cast<long long>(H / Hkv) * T;
   s.pairs = (s.rows + 255) / 256;
-  s.piece_rows = s.rows <= 128 ? 2 * s.rows : 256;
+  s.piece_rows = s.rows <= 128 ? 2 * fa::tree_copies(static_cast<int>(s.rows)) * s.rows : 256;
   s.pieces = fa::kTreeMaxGrid + static_cast<long long>(B) * Hkv * s.pairs;
   return s;
 }
@@ -736,7 +736,7 @@ fa_status tree_impl(const void* Q, const void* K_cache, const void* V_cache, voi
   a.stats = reinterpret_cast<float2*>(ws + round256(slots * d * 4));
   a.prefix_out = reinterpret_cast<int*>(ws + round256(slots * d * 4) + round256(slots * 8));
   CUtensorMap tmQ, tmK, tmV;
-  FA_TRY(make_tmap(&tmQ, Q, B * Hkv, a.rows, d));
+  FA_TRY(make_tmap(&tmQ, Q, B * Hkv, a.rows, d, 128 / fa::tree_copies(a.rows)));
   // (without a page there is no token to load: any valid address does)
   const void* kc = num_pages > 0 ? K_cache : Q;
   const void* vc = num_pages > 0 ? V_cache : Q;

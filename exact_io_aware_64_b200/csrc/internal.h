@@ -151,6 +151,8 @@ cudaError_t launch_rotary(const RotaryArgs& a, int elem_bytes, int num_sms, cuda
 // Attention of few query rows per sequence over a paged cache (tree_sm100.cu).
 constexpr int kTreeMaxBatch = 4096;  // the tile-count prefix sums live in shared memory
 constexpr int kTreeMaxGrid = 148;    // CTAs of the split (one per SM of a B200)
+// Copies of a key head's rows in its 128-row tile (see tree_sm100.cu).
+constexpr int tree_copies(int rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
 struct TreeArgs {
   unsigned int* err;
   const int* block_table;  // [B][max_pages]

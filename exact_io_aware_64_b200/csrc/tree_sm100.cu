@@ -27,6 +27,13 @@
 // With more than 128 rows the two warpgroups own a row tile each and both see every key
 // tile; otherwise they own the same rows and take the key tiles in turn.  A warp none of
 // whose rows exist only passes the barriers.
+//
+// With at most 64 (32) rows the row tile holds 2 (4) copies of them, and the warps of copy c
+// take the c-th part of a key tile's columns: their probabilities elsewhere are zero, so each
+// copy accumulates the output of its own keys, with its own maximum and sum, and is one more
+// part for the joining kernel.  A single warp going through 128 columns takes longer than
+// the tile's share of the HBM rate (1.7 us against 1.5 us a tile, 2.2 us capped); 32 columns
+// each do not.
 #include <cstdint>
 
 #include "internal.h"
@@ -122,7 +129,7 @@ struct KernelArgs : TreeArgs {
   CapArgs cap;
 };
 
-template <int D, bool kCap>
+template <int D, bool kCap, int kCopies>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_sm100_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmK,
@@ -197,11 +204,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int end = min(total, begin + share);
   if (blockIdx.x == 0)  // the joining kernel reads the line's layout from here
     for (int b = threadIdx.x; b <= a.B; b += kThreads) a.prefix_out[b] = prefix[b];
+  // the joining kernel may be launched: it waits for this one's end by itself
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = *tmem_slot;
   const uint32_t tS[2] = {tmem, tmem + 128};
   const uint32_t tO[2] = {tmem + 256, tmem + 256 + D};
   // one row tile: the two warpgroups share its rows and take the key tiles in turn
-  const bool shared_rows = a.rows <= kBM;
+  const bool shared_rows = kCopies > 1 || a.rows <= kBM;
+  constexpr int kCopyRows = kBM / kCopies;  // rows of a copy in the row tile
+  constexpr int kCols = kBN / kCopies;      // key columns of a warp
 
   if (warp >= 8) regs_dec<kRegsControl>();
   if (warp == kWarpTMA) {
@@ -213,23 +224,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t issued_phase[L::kStages];
     for (int s = 0; s < L::kStages; ++s) issued[s] = 0, issued_phase[s] = 0;
     const int box = min(a.page, kBN);  // rows of one load: a page, or a tile of a larger one
-    auto load = [&](const Unit& u, int j, const CUtensorMap* tm) -> bool {
+    // this lane's page of key tile j: lane p fetches the tile's box p.  Read a tile ahead of
+    // its use, so that the loads do not wait for the table.
+    auto boxes = [&](const Unit& u, int j) { return min(kBN / box, (u.len - j * kBN + box - 1) / box); };
+    auto page_of = [&](const Unit& u, int j) -> int {
+      if (j >= u.j1 || lane >= boxes(u, j)) return 0;
+      return a.block_table[static_cast<size_t>(u.b) * a.max_pages + (j * kBN + lane * box) / a.page];
+    };
+    auto load = [&](const Unit& u, int j, int id, const CUtensorMap* tm) -> bool {
       if (!wait_warp(bar(L::kBarKVEmpty + stage), phase ^ 1)) return false;
-      // the boxes of this tile that hold tokens; lane p fetches box p
-      const int boxes = min(kBN / box, (u.len - j * kBN + box - 1) / box);
+      const int n = boxes(u, j);
       const uint32_t fb = bar(L::kBarKVFull + stage);
-      mbar_arrive_expect_tx_elect(fb, boxes * box * D * 2);
+      mbar_arrive_expect_tx_elect(fb, n * box * D * 2);
       __syncwarp();
-      if (lane < boxes) {
-        const int tok = j * kBN + lane * box;
-        int id = a.block_table[static_cast<size_t>(u.b) * a.max_pages + tok / a.page];
+      if (lane < n) {
         if (id < 0 || id >= a.num_pages) {
           atomicOr(a.err, kErrBadPage);
           id = 0;
         }
         const uint32_t dst = base + L::kRing + stage * L::kTileBytes + lane * box * 128;
         for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(dst + c * L::kBoxBytes, tm, fb, c * 64, tok % a.page, id * a.Hkv + u.head);
+          tma_load_3d(dst + c * L::kBoxBytes, tm, fb, c * 64, (j * kBN + lane * box) % a.page,
+                      id * a.Hkv + u.head);
       }
       __syncwarp();
       issued[stage] = 1;
@@ -245,15 +261,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive_expect_tx_elect(bar(L::kBarQFull), row_tiles * L::kTileBytes);
       for (int t = 0; t < row_tiles; ++t)
         for (int c = 0; c < D / 64; ++c)
-          tma_load_3d_elect(base + L::kQ + t * L::kTileBytes + c * L::kBoxBytes, &tmQ,
-                            bar(L::kBarQFull), c * 64, (u.rt + t) * kBM, u.b * a.Hkv + u.head);
+          for (int k = 0; k < kCopies; ++k)  // (a box is kCopyRows rows high)
+            tma_load_3d_elect(base + L::kQ + t * L::kTileBytes + c * L::kBoxBytes +
+                                  k * kCopyRows * 128,
+                              &tmQ, bar(L::kBarQFull), c * 64, (u.rt + t) * kBM,
+                              u.b * a.Hkv + u.head);
       ++units;
       // order of use: K V K V ... (a row tile each), or K K V K V ... V V (shared rows)
-      const int ahead = shared_rows ? 2 : 1;
-      for (int j = u.j0; ok && j < min(u.j1, u.j0 + ahead - 1); ++j) ok = load(u, j, &tmK);
+      // (V's page is K's; `id` holds tiles j and j + 1, read before tile j's waits)
+      int id = page_of(u, u.j0), id1 = page_of(u, u.j0 + 1);
+      if (shared_rows) ok = load(u, u.j0, id, &tmK);
       for (int j = u.j0; ok && j < u.j1; ++j) {
-        if (j + ahead - 1 < u.j1) ok = load(u, j + ahead - 1, &tmK);
-        if (ok) ok = load(u, j, &tmV);
+        const int id2 = page_of(u, j + 2);
+        if (!shared_rows)
+          ok = load(u, j, id, &tmK);
+        else if (j + 1 < u.j1)
+          ok = load(u, j + 1, id1, &tmK);
+        if (ok) ok = load(u, j, id, &tmV);
+        id = id1;
+        id1 = id2;
       }
       pos += u.j1 - u.j0;
     }
@@ -351,11 +377,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (more) issue_s(1, 1, ks);
         }
+        // (the unit's last score product is issued: the next unit's rows may be loaded)
+        if (i + lead == n - 1 || (i == 0 && n <= lead)) mma_commit_elect(bar(L::kBarQEmpty));
         mma_commit_elect(bar(L::kBarKVEmpty + vs));
         if (ks >= 0) mma_commit_elect(bar(L::kBarKVEmpty + ks));
       }
       if (!ok) break;
-      mma_commit_elect(bar(L::kBarQEmpty));
       ++o_uses[0];
       if (two || (shared_rows && n > 1)) ++o_uses[1];
       pos += n;
@@ -365,7 +392,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 8) {
     regs_inc<kRegsSoftmax>();
     const int t = warp / 4;
-    const int row = (warp % 4) * 32 + lane;
+    const int copy = (warp % 4) * 32 / kCopyRows;
+    const int row0 = (warp % 4) * 32 % kCopyRows;  // the warp's first row of its copy
+    const int row = row0 + lane;
+    const int col0 = copy * kCols;
     const uint32_t lane_off = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t tSrow = tS[t] + lane_off, tOrow = tO[t] + lane_off;
     int s_count = 0, o_count = 0;
@@ -379,15 +409,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tile = u.rt + (shared_rows ? 0 : t);
       const int m_row = tile * kBM + row;
       const int i0 = shared_rows ? t : 0, step = shared_rows ? 2 : 1;
-      // the workspace keeps a row of each warpgroup per piece (shared rows), or a row tile's
+      // the workspace keeps a piece's rows once per warpgroup and copy (shared rows), or two
+      // row tiles
       const size_t slot = static_cast<size_t>(u.piece) * a.piece_rows +
-                          (shared_rows ? t * a.rows : t * kBM) + row;
+                          (shared_rows ? (t * kCopies + copy) * a.rows : t * kBM) + row;
       if (tile * kBM >= a.rows || i0 >= n) {
         // (shared rows, one key tile: this warpgroup's part of the piece is empty)
         if (shared_rows && m_row < a.rows) a.stats[slot] = make_float2(-INFINITY, 0.f);
         continue;
       }
-      const bool active = tile * kBM + (warp % 4) * 32 < a.rows;
+      const bool active = tile * kBM + row0 < a.rows;
       const int tok = m_row % a.T;
       unsigned long long bits = 0;  // drafted tokens that this row sees
       if (m_row < a.rows && tok < u.n) {
@@ -407,25 +438,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         tc_fence_after();
-        float s[kBN];
+        float s[kCols];
         {
-          uint32_t sr[kBN];
+          uint32_t sr[kCols];
 #pragma unroll
-          for (int c = 0; c < kBN / 32; ++c) tmem_ld32(tSrow + c * 32, &sr[c * 32]);
+          for (int c = 0; c < kCols / 32; ++c) tmem_ld32(tSrow + col0 + c * 32, &sr[c * 32]);
           tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < kBN; ++c) s[c] = __uint_as_float(sr[c]);
+          for (int c = 0; c < kCols; ++c) s[c] = __uint_as_float(sr[c]);
         }
-        const int kv0 = (u.j0 + i) * kBN;
+        const int kv0 = (u.j0 + i) * kBN + col0;
         // log2-unit score of entry c: s[c] * unit, or (capped) s[c] q(s[c]^2)
         float unit = a.scale_log2, amax = 0.f;
         bool capped = false;
-        const bool tail = kv0 + kBN > u.ctx;
+        const bool tail = kv0 + kCols > u.ctx;
         // drafted tokens are seen by their bits; slots behind the sequence's end have none
         auto hide = [&](float value) {
           if (!tail) return;
 #pragma unroll
-          for (int q = 0; q < kBN / 32; ++q) {
+          for (int q = 0; q < kCols / 32; ++q) {
             const uint32_t w = seen_word(bits, kv0 + 32 * q - u.ctx);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
@@ -434,14 +465,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if constexpr (kCap) {
           hide(0.f);  // (what lies behind the end does not choose the form)
-          amax = abs_max<kBN>(s);
+          amax = abs_max<kCols>(s);
           const bool over = cap_over(amax, a.cap);
           capped = !tail && !over;
           if (!capped) {
             if (seldom(over))
-              cap_scores_any<kBN>(s, a.cap);
+              cap_scores_any<kCols>(s, a.cap);
             else
-              cap_scores<kBN>(s, a.cap);
+              cap_scores<kCols>(s, a.cap);
             unit = 1.f;
           }
         }
@@ -454,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 8; ++k) mx8[k] = s[k];
 #pragma unroll
-          for (int c = 8; c < kBN; c += 2)
+          for (int c = 8; c < kCols; c += 2)
             mx8[(c / 2) % 8] = max3(mx8[(c / 2) % 8], s[c], s[c + 1]);
           m_tile = unit * max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]),
                                fmaxf(mx8[6], mx8[7]));
@@ -483,12 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         l *= alpha;
         const float mref = (m == -INFINITY) ? 0.f : m;
-        uint32_t pk[kBN / 2];
+        uint32_t pk[kCols / 2];
         const uint64_t unit2 = f32x2(unit, unit), negm2 = f32x2(-mref, -mref);
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
         if (kCap && capped) {
 #pragma unroll
-          for (int c = 0; c < kBN / 2; ++c) {
+          for (int c = 0; c < kCols / 2; ++c) {
             const uint64_t s2 = f32x2(s[2 * c], s[2 * c + 1]);
             float p0, p1;
             exp2_pair(fma_x2(s2, cap_factor(s2, a.cap), negm2), p0, p1);
@@ -497,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
 #pragma unroll
-          for (int c = 0; c < kBN / 2; ++c) {
+          for (int c = 0; c < kCols / 2; ++c) {
             float p0, p1;
             exp2_pair(fma_x2(f32x2(s[2 * c], s[2 * c + 1]), unit2, negm2), p0, p1);
             ls2[c % 4] = add_x2(ls2[c % 4], f32x2(p0, p1));
@@ -508,8 +539,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) f32x2_split(ls2[k], ls[2 * k], ls[2 * k + 1]);
         l += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
-        tmem_st32(tSrow, &pk[0]);
-        tmem_st32(tSrow + 32, &pk[32]);
+        if constexpr (kCopies == 1) {
+          tmem_st32(tSrow, &pk[0]);
+          tmem_st32(tSrow + 32, &pk[32]);
+        } else {
+          // (16 columns of the operand hold 32 keys; the other copies' keys are zeros here)
+          uint32_t zero[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) zero[k] = 0u;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            constexpr int kOwn = kCols / 32;
+            if (k / kOwn != copy) tmem_st16(tSrow + 16 * k, zero);
+          }
+#pragma unroll
+          for (int k = 0; k < kCols / 32; ++k)
+            tmem_st16(tSrow + col0 / 2 + 16 * k, &pk[16 * k]);
+        }
         tmem_wait_st();
         warp_arrive(bar(L::kBarPReady + t));
       }
@@ -549,85 +595,114 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the pieces of one row per block: with M the largest maximum,
-// O = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p.  Warps take the pieces in turn
-// (their loads are independent); the sums are added in warp order.
-constexpr int kJoinThreads = 128;
-constexpr int kJoinWarps = kJoinThreads / 32;
+// Joins the parts of one row per block: with M the largest maximum,
+// O = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p.  Bound by latency: the D / 4 lanes of
+// a group go through the group's parts in one pass with a running maximum, kBatch parts'
+// statistics and output rows (16 bytes a lane) in flight together, and the groups' results
+// are joined in a fixed order.  Few rows take 256 threads each (a long sequence's row has
+// hundreds of parts); from kManyRows rows on, whose sequences share the SMs and have few
+// parts, 64 threads each.  It is launched while the first kernel runs and waits for its
+// results on the device.
+constexpr int kManyRows = 1024;
+constexpr int kBatch = 4;
 
-template <int D>
+template <int D, int kJoinThreads>
 __global__ void __launch_bounds__(kJoinThreads)
-    tree_join_kernel(const TreeArgs a, __nv_bfloat16* O, float* LSE, int grid) {
-  __shared__ float red_m[kJoinWarps], red_l[kJoinWarps];
-  __shared__ float red_o[kJoinWarps][D];
-  constexpr int kE = D / 32;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    tree_join_kernel(const TreeArgs a, __nv_bfloat16* O, float* LSE, int grid, int copies) {
+  constexpr int kLanes = D / 4;                    // threads of one part's row
+  constexpr int kGroups = kJoinThreads / kLanes;   // parts read at once
+  __shared__ float2 red_s[kGroups];
+  __shared__ float4 red_o[kGroups][kLanes];
   const long long out_row = blockIdx.x;  // row of [B][Hkv][rows]
   const int r = static_cast<int>(out_row % a.rows);
   const int bh = static_cast<int>(out_row / a.rows);
   const int b = bh / a.Hkv, head = bh % a.Hkv;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = a.seqlens_q != nullptr ? a.seqlens_q[b] : a.T;
   const int len = a.cache_lens[b];
+  const int before = a.prefix_out[b], after = a.prefix_out[b + 1], total = a.prefix_out[a.B];
   // a row behind the sequence's drafted tokens, or of a sequence out of range: left alone
   if (len < 0 || len > a.max_len || n < 0 || n > a.T || n > len || r % a.T >= n) return;
   const bool shared_rows = a.rows <= kBM;
   const int per_seq = a.Hkv * a.pairs;
-  const int total = a.prefix_out[a.B];
   const int share = (total + grid - 1) / grid;
-  const int tiles = (a.prefix_out[b + 1] - a.prefix_out[b]) / per_seq;
+  const int tiles = (after - before) / per_seq;
   const int seg = head * a.pairs + r / (2 * kBM);
-  const int first = a.prefix_out[b] + seg * tiles;  // the segment on the line
+  const int first = before + seg * tiles;  // the segment on the line
   const int c0 = first / share, c1 = (first + tiles - 1) / share;
-  const int parts = (c1 - c0 + 1) * (shared_rows ? 2 : 1);
-  auto slot = [&](int p) {
-    const int c = c0 + (shared_rows ? p / 2 : p);
-    return static_cast<size_t>(c + b * per_seq + seg) * a.piece_rows +
-           (shared_rows ? (p & 1) * a.rows + r : r % (2 * kBM));
-  };
-  float M = -INFINITY;
-  for (int p = threadIdx.x; p < parts; p += kJoinThreads) M = fmaxf(M, a.stats[slot(p)].x);
+  const int per_piece = shared_rows ? 2 * copies : 1;  // warpgroups x copies of the rows
+  const int parts = (c1 - c0 + 1) * per_piece;
+  // part p's row: the rows of a piece's parts follow one another, and so do pieces
+  const size_t row0 = static_cast<size_t>(c0 + b * per_seq + seg) * a.piece_rows +
+                      (shared_rows ? r : r % (2 * kBM));
+  const int step = shared_rows ? a.rows : a.piece_rows;
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p0 = group; p0 < parts; p0 += kGroups * kBatch) {
+    float2 st[kBatch];
+    float4 v[kBatch];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) red_m[warp] = M;
+    for (int k = 0; k < kBatch; ++k) {
+      const int p = p0 + k * kGroups;
+      st[k] = make_float2(-INFINITY, 0.f);
+      if (p < parts) {
+        const size_t at = row0 + static_cast<size_t>(p) * step;
+        st[k] = a.stats[at];
+        v[k] = *reinterpret_cast<const float4*>(a.parts + at * D + lane * 4);
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) top = fmaxf(top, st[k].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float alpha = ex2_approx(m - ref);
+    acc.x *= alpha, acc.y *= alpha, acc.z *= alpha, acc.w *= alpha;
+    l *= alpha;
+    m = top;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      // (an empty part has -inf and 0; its output row may never have been written)
+      if (st[k].y == 0.f) continue;
+      const float w = ex2_approx(st[k].x - ref);
+      l = fmaf(w, st[k].y, l);
+      acc.x = fmaf(w, v[k].x, acc.x);
+      acc.y = fmaf(w, v[k].y, acc.y);
+      acc.z = fmaf(w, v[k].z, acc.z);
+      acc.w = fmaf(w, v[k].w, acc.w);
+    }
+  }
+  if (lane == 0) red_s[group] = make_float2(m, l);
+  red_o[group][lane] = acc;
   __syncthreads();
-  M = red_m[0];
+  if (threadIdx.x >= kLanes) return;
+  float M = red_s[0].x;
 #pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) M = fmaxf(M, red_m[w]);
+  for (int g = 1; g < kGroups; ++g) M = fmaxf(M, red_s[g].x);
   const float ref = M == -INFINITY ? 0.f : M;
-  float l = 0.f, acc[kE] = {};
-  for (int p = warp; p < parts; p += kJoinWarps) {
-    const size_t at = slot(p);
-    const float2 st = a.stats[at];
-    if (st.x == -INFINITY && st.y == 0.f) continue;  // empty: its output may be unwritten
-    const float w = ex2_approx(st.x - ref);
-    l = fmaf(w, st.y, l);
-    const float* src = a.parts + at * D + lane * kE;
+  l = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int e = 0; e < kE; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+  for (int g = 0; g < kGroups; ++g) {
+    const float w = ex2_approx(red_s[g].x - ref);
+    const float4 v = red_o[g][lane];
+    l = fmaf(w, red_s[g].y, l);
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
   }
-  if (lane == 0) red_l[warp] = l;
-#pragma unroll
-  for (int e = 0; e < kE; ++e) red_o[warp][lane * kE + e] = acc[e];
-  __syncthreads();
-  l = red_l[0];
-#pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) l += red_l[w];
   const float inv = l == 0.f ? 0.f : 1.f / l;  // (a row that sees no key: 0 and -inf)
-  const size_t dst = static_cast<size_t>(out_row);
-  for (int e = threadIdx.x; e < D; e += kJoinThreads) {
-    float x = red_o[0][e];
-#pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) x += red_o[w][e];
-    O[dst * D + e] = __float2bfloat16_rn(x * inv);
-  }
-  if (LSE != nullptr && threadIdx.x == 0)
-    LSE[dst] = l == 0.f ? -INFINITY : (ref + __log2f(l)) * 0.69314718055994531f;
+  *reinterpret_cast<uint2*>(O + static_cast<size_t>(out_row) * D + lane * 4) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (LSE != nullptr && lane == 0)
+    LSE[out_row] = l == 0.f ? -INFINITY : (ref + __log2f(l)) * 0.69314718055994531f;
 }
 
-template <int D, bool kCap>
+template <int D, bool kCap, int kCopies>
 cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                      void* O, float* LSE, const TreeArgs& a, int num_sms, cudaStream_t stream) {
-  auto* kernel = tree_sm100_kernel<D, kCap>;
+  auto* kernel = tree_sm100_kernel<D, kCap, kCopies>;
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = ready_kernel(kernel, kRegsLaunch, Layout<D>::bytes(kTreeMaxBatch), ready);
   if (e != cudaSuccess) return e;
@@ -637,9 +712,18 @@ cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   kernel<<<num_sms, kThreads, Layout<D>::bytes(a.B), stream>>>(tmQ, tmK, tmV, ka);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const long long rows = static_cast<long long>(a.B) * a.Hkv * a.rows;
-  tree_join_kernel<D><<<static_cast<unsigned>(rows), kJoinThreads, 0, stream>>>(
-      a, static_cast<__nv_bfloat16*>(O), LSE, num_sms);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows));
+  const int threads = rows < kManyRows ? 256 : 64;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, threads == 256 ? tree_join_kernel<D, 256> : tree_join_kernel<D, 64>,
+                            a, static_cast<__nv_bfloat16*>(O), LSE, num_sms, kCopies);
 }
 
 }  // namespace
@@ -647,10 +731,21 @@ cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
 cudaError_t launch_tree_sm100(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                               const CUtensorMap& tmV, void* O, float* LSE, const TreeArgs& a,
                               int d, int num_sms, cudaStream_t stream) {
-  const bool cap = a.softcap > 0.f;
   auto launch = [&](auto* k) { return k(tmQ, tmK, tmV, O, LSE, a, num_sms, stream); };
-  if (d == 64) return cap ? launch(launch_t<64, true>) : launch(launch_t<64, false>);
-  return cap ? launch(launch_t<128, true>) : launch(launch_t<128, false>);
+  switch (tree_copies(a.rows) * 4 + (d == 128) * 2 + (a.softcap > 0.f)) {
+    case 4: return launch(launch_t<64, false, 1>);
+    case 5: return launch(launch_t<64, true, 1>);
+    case 6: return launch(launch_t<128, false, 1>);
+    case 7: return launch(launch_t<128, true, 1>);
+    case 8: return launch(launch_t<64, false, 2>);
+    case 9: return launch(launch_t<64, true, 2>);
+    case 10: return launch(launch_t<128, false, 2>);
+    case 11: return launch(launch_t<128, true, 2>);
+    case 16: return launch(launch_t<64, false, 4>);
+    case 17: return launch(launch_t<64, true, 4>);
+    case 18: return launch(launch_t<128, false, 4>);
+    default: return launch(launch_t<128, true, 4>);
+  }
 }
 
 }  // namespace fa
