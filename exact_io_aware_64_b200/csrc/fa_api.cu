@@ -134,6 +134,25 @@ fa_status make_tmap_packed(CUtensorMap* tm, const void* ptr, int tokens, int H, 
   return FA_OK;
 }
 
+// [pages][page][d] bf16 (pages: page number x key head) viewed as a 5-D tensor of (64
+// columns, 8 rows, column halves, 8-row groups, pages); boxes of `rows` rows x all columns,
+// 128-byte swizzle.
+fa_status make_tmap_pages(CUtensorMap* tm, const void* ptr, int pages, int page, int d, int rows) {
+  auto fn = encode_fn();
+  if (!fn) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
+  cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(d / 64), static_cast<cuuint64_t>(page / 8),
+                        static_cast<cuuint64_t>(pages)};
+  cuuint64_t strides[4] = {row, 128, 8 * row, static_cast<cuuint64_t>(page) * row};
+  cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(d / 64), static_cast<cuuint32_t>(rows / 8), 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
+  return FA_OK;
+}
+
 // [BH][rows] float32 (a per-row statistic padded to whole tiles) viewed as a 3-D tensor
 // [1][BH][rows] with boxes of 128 rows, no swizzle.
 fa_status make_row_tmap(CUtensorMap* tm, const float* ptr, int BH, int rows) {
@@ -741,8 +760,8 @@ fa_status tree_impl(const void* Q, const void* K_cache, const void* V_cache, voi
   const void* kc = num_pages > 0 ? K_cache : Q;
   const void* vc = num_pages > 0 ? V_cache : Q;
   const int box = page < 128 ? page : 128;
-  FA_TRY(make_tmap(&tmK, kc, num_pages > 0 ? num_pages * Hkv : 1, page, d, box));
-  FA_TRY(make_tmap(&tmV, vc, num_pages > 0 ? num_pages * Hkv : 1, page, d, box));
+  FA_TRY(make_tmap_pages(&tmK, kc, num_pages > 0 ? num_pages * Hkv : 1, page, d, box));
+  FA_TRY(make_tmap_pages(&tmV, vc, num_pages > 0 ? num_pages * Hkv : 1, page, d, box));
   const int grid = dev.num_sms < fa::kTreeMaxGrid ? dev.num_sms : fa::kTreeMaxGrid;
   cudaError_t e = fa::launch_tree_sm100(tmQ, tmK, tmV, O, LSE, a, d, grid, stream);
   if (e != cudaSuccess) return cuda_fail(e, "launching the tree-attention kernels");

@@ -169,6 +169,16 @@ __device__ __forceinline__ void tma_load_3d_elect(uint32_t smem_dst, const void*
       : "memory");
 }
 
+// 5-D tiled load of one box.
+__device__ __forceinline__ void tma_load_5d(uint32_t smem_dst, const void* tmap, uint32_t bar,
+                                            int c0, int c1, int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_dst),
+      "l"(tmap), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+
 // 3-D tiled store of one box from shared memory to global memory, tracked in the issuing
 // thread's bulk async-group.  The box's shared-memory bytes must have been written and
 // made visible to the async proxy (fence_proxy_async_shared) before the store is issued.
