@@ -230,29 +230,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     int issued[L::kStages];
     uint32_t issued_phase[L::kStages];
     for (int s = 0; s < L::kStages; ++s) issued[s] = 0, issued_phase[s] = 0;
-    const int box = min(a.page, kBN);  // rows of one load: a page, or a tile of a larger one
-    // this lane's page of key tile j: lane p fetches the tile's box p.  Read a tile ahead of
-    // its use, so that the loads do not wait for the table.
-    auto boxes = [&](const Unit& u, int j) { return min(kBN / box, (u.len - j * kBN + box - 1) / box); };
-    auto page_of = [&](const Unit& u, int j) -> int {
-      if (j >= u.j1 || lane >= boxes(u, j)) return 0;
-      return a.block_table[static_cast<size_t>(u.b) * a.max_pages + (j * kBN + lane * box) / a.page];
-    };
-    auto load = [&](const Unit& u, int j, int id, const CUtensorMap* tm) -> bool {
+    // This warp paces short tiles (with divisions and a table read per load it took 2060
+    // cycles a tile, which held a d = 64 batch of 64 x 8192 tokens to 135 us; 101 as it is),
+    // so it divides and reads the table seldom.  Pages below 128
+    // tokens are a power of two: a tile is `per` boxes of a page each, lane p fetching box p;
+    // larger pages hold `tiles` tiles of one box each.
+    const bool small = a.page < kBN;
+    const int page_sh = small ? 31 - __clz(a.page) : 7;  // log2 of a box's rows
+    const int per = kBN >> page_sh, tiles = small ? 1 : a.page / kBN;
+    const uint32_t box_bytes = static_cast<uint32_t>(D * 2) << page_sh;
+    auto load = [&](const Unit& u, int j, int id, int tile_in_page, const CUtensorMap* tm) -> bool {
       if (!wait_warp(bar(L::kBarKVEmpty + stage), phase ^ 1)) return false;
-      const int n = boxes(u, j);
+      // the boxes of this tile that hold tokens
+      const int n = min(per, (u.len - j * kBN + (1 << page_sh) - 1) >> page_sh);
       const uint32_t fb = bar(L::kBarKVFull + stage);
-      mbar_arrive_expect_tx_elect(fb, n * box * D * 2);
+      if (lane == 0) mbar_arrive_expect_tx(fb, n * box_bytes);
       __syncwarp();
-      if (lane < n) {
-        if (id < 0 || id >= a.num_pages) {
-          atomicOr(a.err, kErrBadPage);
-          id = 0;
-        }
-        tma_load_5d(base + L::kRing + stage * L::kTileBytes + lane * box * D * 2, tm, fb, 0, 0, 0,
-                    (j * kBN + lane * box) % a.page / 8, id * a.Hkv + u.head);
-      }
-      __syncwarp();
+      if (lane < n)
+        tma_load_5d(base + L::kRing + stage * L::kTileBytes + lane * box_bytes, tm, fb, 0, 0, 0,
+                    tile_in_page * (kBN / 8), id * a.Hkv + u.head);
       issued[stage] = 1;
       issued_phase[stage] = phase;
       if (++stage == L::kStages) stage = 0, phase ^= 1;
@@ -260,6 +256,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int pos = begin; ok && pos < end;) {
       const Unit u = tree_unit(a, prefix, pos, end);
+      // page numbers: a lane holds one of 32 table entries from entry `win` on, and one of
+      // the next 32; tile j's entries are e, e + 1, ..
+      const int* table = a.block_table + static_cast<size_t>(u.b) * a.max_pages;
+      int e = small ? u.j0 * per : u.j0 / tiles;
+      int in_page = small ? 0 : u.j0 - e * tiles;
+      const int e_end = small ? (min(u.len, u.j1 * kBN) + a.page - 1) >> page_sh
+                              : (u.j1 - 1) / tiles + 1;
+      auto entry = [&](int i) { return i < e_end ? table[i] : 0; };
+      int win = e;
+      int ids = entry(win + lane), ids_next = entry(win + 32 + lane);
       if (units > 0) ok = wait_warp(bar(L::kBarQEmpty), (units - 1) & 1);
       if (!ok) break;
       const int row_tiles = min(2, (a.rows - u.rt * kBM + kBM - 1) / kBM);
@@ -272,19 +278,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                               &tmQ, bar(L::kBarQFull), c * 64, (u.rt + t) * kBM,
                               u.b * a.Hkv + u.head);
       ++units;
+      auto next_page = [&](int& tile_in_page) -> int {
+        if (e - win == 32) {
+          win += 32;
+          ids = ids_next;
+          ids_next = entry(win + 32 + lane);
+        }
+        int id = __shfl_sync(0xffffffffu, ids, (e - win + (lane & (per - 1))) & 31);
+        if (id < 0 || id >= a.num_pages) {  // (entries behind the last token's page are 0 here)
+          atomicOr(a.err, kErrBadPage);
+          id = 0;
+        }
+        tile_in_page = in_page;
+        if (small) {
+          e += per;
+        } else if (++in_page == tiles) {
+          in_page = 0;
+          ++e;
+        }
+        return id;
+      };
       // order of use: K V K V ... (a row tile each), or K K V K V ... V V (shared rows)
-      // (V's page is K's; `id` holds tiles j and j + 1, read before tile j's waits)
-      int id = page_of(u, u.j0), id1 = page_of(u, u.j0 + 1);
-      if (shared_rows) ok = load(u, u.j0, id, &tmK);
+      int o0, o1 = 0;
+      int id0 = next_page(o0), id1 = 0;
+      ok = load(u, u.j0, id0, o0, &tmK);
       for (int j = u.j0; ok && j < u.j1; ++j) {
-        const int id2 = page_of(u, j + 2);
-        if (!shared_rows)
-          ok = load(u, j, id, &tmK);
-        else if (j + 1 < u.j1)
-          ok = load(u, j + 1, id1, &tmK);
-        if (ok) ok = load(u, j, id, &tmV);
-        id = id1;
-        id1 = id2;
+        const bool more = j + 1 < u.j1;
+        if (more) id1 = next_page(o1);
+        if (shared_rows && more) ok = load(u, j + 1, id1, o1, &tmK);
+        if (ok) ok = load(u, j, id0, o0, &tmV);
+        if (ok && !shared_rows && more) ok = load(u, j + 1, id1, o1, &tmK);
+        id0 = id1;
+        o0 = o1;
       }
       pos += u.j1 - u.j0;
     }
