@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       // modified scores: this row's visible keys, the keys that every row of the tile
-      // sees, and the head's slope (log2 units, negated)
+      // sees, and the head's slope (negated, in the units of s)
       RowLimits lim_row{0, 0};
       int full_lo = 0, full_hi = 0;
       float neg_slope = 0.f;
@@ -607,7 +607,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         lim_row = mod_row(args.mod, b, min(q_row, last), ui.off, args.Nk, args.causal);
         full_lo = mod_row(args.mod, b, last, ui.off, args.Nk, args.causal).lo;
         full_hi = mod_row(args.mod, b, first, ui.off, args.Nk, args.causal).hi;
-        if constexpr (has_bias(kMode)) neg_slope = args.mod.slopes[ui.h] * -kLog2e;
+        if constexpr (has_bias(kMode)) {
+          neg_slope = args.mod.slopes[ui.h] * -kLog2e;
+          if (!has_cap(kMode)) neg_slope /= args.scale_log2;
+        }
       }
       float m = -INFINITY;  // running max, log2 units (scaled logits * log2 e)
       float l = 0.f;
@@ -648,16 +651,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (has_bias(kMode)) {
             // -slope |p - j|, p this row's position
             const float at = static_cast<float>(kv0 - (q_row + ui.off));
-            const uint64_t u2 = f32x2(unit, unit), sl2 = f32x2(neg_slope, neg_slope),
-                           two2 = f32x2(2.f, 2.f);
+            const uint64_t sl2 = f32x2(neg_slope, neg_slope), two2 = f32x2(2.f, 2.f);
             uint64_t d2 = f32x2(at, at + 1.f);
 #pragma unroll
             for (int c = 0; c < kBN; c += 2) {
-              f32x2_split(fma_x2(sl2, abs_x2(d2), mul_x2(f32x2(s[c], s[c + 1]), u2)), s[c],
-                          s[c + 1]);
+              f32x2_split(fma_x2(sl2, abs_x2(d2), f32x2(s[c], s[c + 1])), s[c], s[c + 1]);
               d2 = add_x2(d2, two2);
             }
-            unit = 1.f;
           }
           if (partial) {
 #pragma unroll

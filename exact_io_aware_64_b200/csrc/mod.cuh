@@ -156,22 +156,28 @@ __device__ __forceinline__ RowLimits mod_key(const ModArgs& m, int b, int j, int
 // Work units of documents differ in cost by far more than causal ones, and not in order of
 // their index: the units (n of them, one head's) are ranked by cost(e), dearest first, for
 // the persistent kernels' dealing order.  Called by all `threads` threads of a CTA before
-// its pipelines start; `scratch` is n uint16 of shared memory that a TMA load may write
-// later, `order` n bytes that stay.  A __syncthreads() must follow.
+// its pipelines start; `scratch` is n uint16, rounded up to 16 bytes, of aligned shared memory
+// that a TMA load may write later, `order` n bytes that stay.  A __syncthreads() must follow.
 constexpr int kMaxOrdered = 256;
 
 template <typename Cost>
 __device__ __forceinline__ void order_units(int n, int threads, uint16_t* scratch, uint8_t* order,
                                             const Cost& cost) {
-  for (int e = threadIdx.x; e < n; e += threads)
-    scratch[e] = static_cast<uint16_t>(min(cost(e), 65535));
+  const int n8 = (n + 7) / 8;
+  for (int e = threadIdx.x; e < 8 * n8; e += threads)
+    scratch[e] = e < n ? static_cast<uint16_t>(min(cost(e), 65535)) : 0;
   __syncthreads();
   for (int e = threadIdx.x; e < n; e += threads) {
     const int c = scratch[e];
     int rank = 0;
-    for (int k = 0; k < n; ++k) {
-      const int o = scratch[k];
-      rank += o > c || (o == c && k < e);
+    for (int g = 0; g < n8; ++g) {  // eight costs a load; equal ones keep their order
+      const uint4 v = reinterpret_cast<const uint4*>(scratch)[g];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int o = (w[k / 2] >> (16 * (k % 2))) & 0xffff;
+        rank += o > c || (o == c && 8 * g + k < e);
+      }
     }
     order[rank] = static_cast<uint8_t>(e);
   }

@@ -12,11 +12,16 @@
 // pair), so it must not be repeated for every head.
 //
 // Vector form (R, strides and pointers allow 16-byte pieces): a thread owns one piece of a
-// head row at one token, forms its 2 to 8 angles once, in registers, and turns that piece
-// of every head of Q and K, four heads' loads in flight at a time; neighbouring threads hold
+// head row at one token, forms its 2 to 8 angles once, in registers, and turns that piece of
+// every head of Q and K, four heads' loads in flight at a time (the first four while the
+// angles are formed; angles shared by the block through shared memory took 32.6 us where
+// these take 30.9, B=2 H=16+4 N=8192 d=128 R=64 bf16 interleaved, 168 MB at 83 % of the copy
+// rate: the barrier kept the first loads back); neighbouring threads hold
 // neighbouring pieces, then neighbouring tokens.  With few tokens, threads (then blocks)
-// share a token's heads.  Scalar form (anything else): one pair at a time, the angles in
-// shared memory.
+// share a token's heads.  Calls that move more than kStreamBytes load and store past the L2
+// (B=2 H=16+16 N=4096 d=64 float32, 134 MB: 20.7 us with, 23.8 without; N=2048 H=16+4 d=128
+// bf16, 42 MB, whose output the attention can still find in the L2: 13.4 with, 12.7
+// without).  Scalar form (anything else): one pair at a time.
 #include <cmath>
 #include <cstdint>
 
@@ -30,6 +35,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 16;  // tokens of one block
 constexpr int kUnroll = 4;      // heads whose loads a thread has in flight
+constexpr long long kStreamBytes = 96ll << 20;  // in and out: about the L2's size
 
 // cos and sin (times m) of pair k at flat token tok.
 __device__ __forceinline__ float2 angle(const RotaryArgs& a, double pos, int k) {
@@ -43,6 +49,16 @@ __device__ __forceinline__ float2 angle(const RotaryArgs& a, double pos, int k) 
 __device__ __forceinline__ double position(const RotaryArgs& a, int tok) {
   return a.positions != nullptr ? static_cast<double>(a.positions[tok])
                                 : static_cast<double>(a.first + tok % a.N);
+}
+
+// The block's angles, [n][R/2], from flat token t0 on.
+__device__ __forceinline__ void fill_angles(float2* cs, const RotaryArgs& a, long long t0, int n) {
+  const int half = a.R / 2;
+  for (int i = threadIdx.x; i < n * half; i += kThreads) {
+    const int t = i / half;
+    cs[i] = angle(a, position(a, static_cast<int>(t0) + t), i - t * half);
+  }
+  __syncthreads();
 }
 
 template <typename T>
@@ -92,8 +108,21 @@ __device__ __forceinline__ void turn(float x1, float x2, float2 w, float& y1, fl
   y2 = fmaf(x2, w.x, __fmul_rn(x1, w.y));
 }
 
-template <typename T, bool kInterleaved>
+template <bool kStream>
+__device__ __forceinline__ uint4 get16(const void* p) {
+  const uint4* q = static_cast<const uint4*>(p);
+  return kStream ? __ldcs(q) : *q;
+}
+template <bool kStream>
+__device__ __forceinline__ void put16(void* p, uint4 v) {
+  uint4* q = static_cast<uint4*>(p);
+  if (kStream) __stcs(q, v);
+  else *q = v;
+}
+
+template <typename T, bool kInterleaved, bool kStream>
 __global__ void __launch_bounds__(kThreads) rotary_vector_kernel(const RotaryArgs a) {
+  const long long t0 = static_cast<long long>(blockIdx.x) * a.tokens;
   constexpr int kV = Vec<T>::n;
   constexpr int kAngles = kInterleaved ? kV / 2 : kV;
   const int half = a.R / 2;
@@ -104,16 +133,9 @@ __global__ void __launch_bounds__(kThreads) rotary_vector_kernel(const RotaryArg
   const int t = (threadIdx.x / a.lanes) & (a.tokens - 1);
   const int group = threadIdx.x / (a.lanes * a.tokens);
   const int groups = kThreads / (a.lanes * a.tokens);
-  const long long tok_ll = static_cast<long long>(blockIdx.x) * a.tokens + t;
-  if (q >= pieces || tok_ll >= a.total) return;
-  const int tok = static_cast<int>(tok_ll);
+  if (q >= pieces || t0 + t >= a.total) return;
+  const int tok = static_cast<int>(t0) + t;
   const bool turns = q < turned;
-  float2 w[kAngles];
-  if (turns) {
-    const double pos = position(a, tok);
-#pragma unroll
-    for (int k = 0; k < kAngles; ++k) w[k] = angle(a, pos, q * kAngles + k);
-  }
   const int e1 = turns ? q * kV : a.R + (q - turned) * kV;
   const long long b = tok / a.N, n = tok - b * a.N;
   const int h0 = blockIdx.y * a.heads_per_block;
@@ -123,16 +145,27 @@ __global__ void __launch_bounds__(kThreads) rotary_vector_kernel(const RotaryArg
   const T* src1 = static_cast<const T*>(a.x[1].in) + (b * a.x[1].in_b + n * a.x[1].in_n + e1);
   T* dst0 = static_cast<T*>(a.x[0].out) + (b * a.x[0].out_b + n * a.x[0].out_n + e1);
   T* dst1 = static_cast<T*>(a.x[1].out) + (b * a.x[1].out_b + n * a.x[1].out_n + e1);
-  for (int hb = h0 + group; hb < h1; hb += groups * kUnroll) {
-    uint4 r1[kUnroll], r2[kUnroll];
+  uint4 r1[kUnroll], r2[kUnroll];
+  auto load = [&](int hb) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int h = hb + u * groups;
       if (h >= h1) break;
       const T* p = h < nq ? src0 + h * a.x[0].in_h : src1 + (h - nq) * a.x[1].in_h;
-      r1[u] = *reinterpret_cast<const uint4*>(p);
-      if (!kInterleaved && turns) r2[u] = *reinterpret_cast<const uint4*>(p + half);
+      r1[u] = get16<kStream>(p);
+      if (!kInterleaved && turns) r2[u] = get16<kStream>(p + half);
     }
+  };
+  // the first heads' loads are on their way while the angles are formed
+  load(h0 + group);
+  float2 w[kAngles];
+  if (turns) {
+    const double pos = position(a, tok);
+#pragma unroll
+    for (int k = 0; k < kAngles; ++k) w[k] = angle(a, pos, q * kAngles + k);
+  }
+  for (int hb = h0 + group; hb < h1; hb += groups * kUnroll) {
+    if (hb != h0 + group) load(hb);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int h = hb + u * groups;
@@ -150,24 +183,22 @@ __global__ void __launch_bounds__(kThreads) rotary_vector_kernel(const RotaryArg
           Vec<T>::unpack(r2[u], x2);
 #pragma unroll
           for (int k = 0; k < kAngles; ++k) turn(x1[k], x2[k], w[k], x1[k], x2[k]);
-          *reinterpret_cast<uint4*>(p + half) = Vec<T>::pack(x2);
+          put16<kStream>(p + half, Vec<T>::pack(x2));
         }
         r1[u] = Vec<T>::pack(x1);
       }
-      *reinterpret_cast<uint4*>(p) = r1[u];
+      put16<kStream>(p, r1[u]);
     }
   }
 }
 
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) rotary_scalar_kernel(const RotaryArgs a) {
-  extern __shared__ float2 cs[];  // [tokens][R/2]
+  extern __shared__ __align__(16) float2 cs[];
   const int half = a.R / 2;
   const long long t0 = static_cast<long long>(blockIdx.x) * a.tokens;
   const int n = static_cast<int>(min(static_cast<long long>(a.tokens), a.total - t0));
-  for (int i = threadIdx.x; i < n * half; i += kThreads)
-    cs[i] = angle(a, position(a, static_cast<int>(t0) + i / half), i % half);
-  __syncthreads();
+  fill_angles(cs, a, t0, n);
   const int h0 = blockIdx.y * a.heads_per_block;
   const int hn = min(a.heads_per_block, a.x[0].heads + a.x[1].heads - h0);
   const int per_row = half + (a.copy_rest ? a.d - a.R : 0);  // pairs, then copied elements
@@ -223,18 +254,13 @@ cudaError_t launch_t(const RotaryArgs& args, bool vector, int num_sms, cudaStrea
     split = (heads + a.heads_per_block - 1) / a.heads_per_block;
   }
   const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>(split));
-  if (vector) {
-    if (a.interleaved)
-      rotary_vector_kernel<T, true><<<grid, kThreads, 0, stream>>>(a);
-    else
-      rotary_vector_kernel<T, false><<<grid, kThreads, 0, stream>>>(a);
-  } else {
-    const size_t smem = static_cast<size_t>(tokens) * (a.R / 2) * sizeof(float2);  // <= 32 KB
-    if (a.interleaved)
-      rotary_scalar_kernel<T, true><<<grid, kThreads, smem, stream>>>(a);
-    else
-      rotary_scalar_kernel<T, false><<<grid, kThreads, smem, stream>>>(a);
-  }
+  const size_t smem = vector ? 0 : static_cast<size_t>(tokens) * (a.R / 2) * sizeof(float2);
+  const bool stream_out = 2 * a.total * heads * a.d * static_cast<long long>(sizeof(T)) > kStreamBytes;
+  void (*kernel)(RotaryArgs) =
+      !vector ? (a.interleaved ? rotary_scalar_kernel<T, true> : rotary_scalar_kernel<T, false>)
+      : stream_out ? (a.interleaved ? rotary_vector_kernel<T, true, true> : rotary_vector_kernel<T, false, true>)
+                   : (a.interleaved ? rotary_vector_kernel<T, true, false> : rotary_vector_kernel<T, false, false>);
+  kernel<<<grid, kThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
