@@ -632,19 +632,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // log2-unit score of entry c: s[c] * unit, or (capped) s[c] q(s[c]^2)
         float unit = args.scale_log2;
         float amax = 0.f;
-        bool capped = false;
+        bool capped = false, partial = false;
         if constexpr (kMode != kModNone) {
-          const bool partial = kv0 < full_lo || kv0 + kBN > full_hi;
+          partial = kv0 < full_lo || kv0 + kBN > full_hi;
           if constexpr (has_cap(kMode)) {
             amax = abs_max<kBN>(s);
             const bool over = cap_over(amax, args.mod.cap);
-            capped = !has_bias(kMode) && !partial && !over;
-            if (!capped) {
-              if (seldom(over)) {
-                cap_scores_any<kBN>(s, args.mod.cap);
-              } else {
-                cap_scores<kBN>(s, args.mod.cap);
-              }
+            capped = !has_bias(kMode) && !over;
+            if (seldom(over)) {
+              cap_scores_any<kBN>(s, args.mod.cap);
+              unit = 1.f;
+            } else if (has_bias(kMode)) {
+              cap_scores<kBN>(s, args.mod.cap);
               unit = 1.f;
             }
           }
@@ -659,7 +658,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               d2 = add_x2(d2, two2);
             }
           }
-          if (partial) {
+          // hidden entries: -inf, or (capped) probability 0 below -- their products are
+          // ordinary scores, which the reference maximum may take in
+          if (partial && !capped) {
 #pragma unroll
             for (int q = 0; q < kBN / 32; ++q) {
               const uint32_t w = range_word(lim_row.lo - kv0 - 32 * q, lim_row.hi - kv0 - 32 * q);
@@ -736,7 +737,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t scale2 = f32x2(sc, sc);
         const uint64_t negm2 = f32x2(-mref, -mref);
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
-        if (has_cap(kMode) && !has_bias(kMode) && capped) {
+        if (has_cap(kMode) && !has_bias(kMode) && capped && partial) {
+#pragma unroll
+          for (int q = 0; q < kBN / 32; ++q) {
+            const uint32_t w = range_word(lim_row.lo - kv0 - 32 * q, lim_row.hi - kv0 - 32 * q);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int c = 16 * q + k;
+              const uint64_t s2 = f32x2(s[2 * c], s[2 * c + 1]);
+              float p0, p1;
+              exp2_pair(fma_x2(s2, cap_factor(s2, args.mod.cap), negm2), p0, p1);
+              if (!((w >> (2 * k)) & 1u)) p0 = 0.f;
+              if (!((w >> (2 * k + 1)) & 1u)) p1 = 0.f;
+              ls2[c % 4] = add_x2(ls2[c % 4], f32x2(p0, p1));
+              pk[c] = pack_bf16x2(p0, p1);
+            }
+          }
+        } else if (has_cap(kMode) && !has_bias(kMode) && capped) {
 #pragma unroll
           for (int c = 0; c < kBN / 2; ++c) {
             const uint64_t s2 = f32x2(s[2 * c], s[2 * c + 1]);

@@ -155,7 +155,9 @@ __device__ __forceinline__ RowLimits mod_key(const ModArgs& m, int b, int j, int
 
 // Work units of documents differ in cost by far more than causal ones, and not in order of
 // their index: the units (n of them, one head's) are ranked by cost(e), dearest first, for
-// the persistent kernels' dealing order.  Called by all `threads` threads of a CTA before
+// the persistent kernels' dealing order.  (10000 tokens of 450 to 2550-token documents, d =
+// 128: dK/dV 145 -> 127 us, dQ 107 -> 96; equal documents of 512 tokens on tile bounds, which
+// the index order suits: 72 -> 78 and 57 -> 63.)  Called by all `threads` threads of a CTA before
 // its pipelines start; `scratch` is n uint16, rounded up to 16 bytes, of aligned shared memory
 // that a TMA load may write later, `order` n bytes that stay.  A __syncthreads() must follow.
 constexpr int kMaxOrdered = 256;
