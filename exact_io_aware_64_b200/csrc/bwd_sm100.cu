@@ -371,6 +371,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(L::kBarDrain), 1);
     fence_mbar_init();
   }
+  // the dQ kernel needs nothing of this one and may take the SMs that run out of units (this
+  // kernel starts after bwd_prep has ended, so D and L2 are there for it too)
+  if constexpr (kMode != kModNone) grid_dependents_launch();
   uint8_t* order = smem + L::kOrder;
   if (kMode != kModNone && args.mod.ordered)
     order_units(args.BH / args.mod.Hkv * args.n_kt, kThreads, reinterpret_cast<uint16_t*>(smem),
@@ -1304,6 +1307,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  // launched while the dK/dV kernel ran: what follows in the stream waits for both
+  if constexpr (kMode != kModNone) grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------ host side
@@ -1365,12 +1370,16 @@ cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   if (e != cudaSuccess) return e;
   e = ready_kernel(bwd_dq_kernel<D, kMode>, kRegsLaunch, DqLayout<D>::kAlloc, ready_q);
   if (e != cudaSuccess) return e;
-  bwd_dkdv_kernel<D, kMode><<<grid_kv, kThreads, DkdvLayout<D>::kAlloc, stream>>>(
-      tmQ, tmK, tmV, tmdO, tmL2, tmD, tmdK, tmdV, a_kv);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // (launched early, while bwd_prep runs, this kernel made the step over documents 20 us
+  // longer)
+  e = launch_early(bwd_dkdv_kernel<D, kMode>, dim3(grid_kv), kThreads, DkdvLayout<D>::kAlloc, stream,
+                   false, tmQ, tmK, tmV, tmdO, tmL2, tmD, tmdK, tmdV, a_kv);
+  if (e != cudaSuccess) return e;
   if ((e = trace_mark(p, 2, stream)) != cudaSuccess) return e;
-  bwd_dq_kernel<D, kMode><<<grid_q, kThreads, DqLayout<D>::kAlloc, stream>>>(tmQ, tmK, tmV, tmdO, a_q);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_early(bwd_dq_kernel<D, kMode>, dim3(grid_q), kThreads, DqLayout<D>::kAlloc, stream,
+                   kMode != kModNone && p.trace == nullptr,
+                   tmQ, tmK, tmV, tmdO, a_q);
+  if (e != cudaSuccess) return e;
   return trace_mark(p, 3, stream);
 }
 

@@ -78,6 +78,9 @@ __global__ void __launch_bounds__(kThreads)
     doc_ranges_kernel(const int* __restrict__ ids, int* __restrict__ start,
                       int* __restrict__ end, int N) {
   __shared__ int warp_val[kWarps];
+  // (no early launch of what follows: a forward kernel's CTAs waiting on the SMs took 7 us
+  // more than starting after this one)
+  grid_dependency_wait();
   const size_t row = static_cast<size_t>(blockIdx.y) * N;
   ids += row;
   start += row;
@@ -147,9 +150,11 @@ cudaError_t launch_doc_ranges(const int* ids, int* start, int* end, int B, int N
     const dim3 grid(static_cast<unsigned>((N + kChunk - 1) / kChunk),
                     static_cast<unsigned>(B - b < 65535 ? B - b : 65535));
     const size_t at = static_cast<size_t>(b) * N;
-    doc_ranges_kernel<<<grid, kThreads, 0, stream>>>(ids + at, start + at, end + at, N);
+    const cudaError_t e = launch_early(doc_ranges_kernel, grid, kThreads, 0, stream, true, ids + at,
+                                       start + at, end + at, N);
+    if (e != cudaSuccess) return e;
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 }  // namespace fa

@@ -300,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmV);
     tma_prefetch_desc(&tmO);
   }
+  if constexpr (kMode != kModNone) grid_dependency_wait();
   uint8_t* order = smem + L::kOrder;
   if (kMode != kModNone && args.mod.ordered) {
     order_units(args.BH / args.H * args.n_units, kThreads, reinterpret_cast<uint16_t*>(smem), order,
@@ -909,8 +910,9 @@ cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   if (e != cudaSuccess) return e;
   const int grid = a.total_units < num_sms ? a.total_units : num_sms;
   if ((e = trace_mark(p, 0, stream)) != cudaSuccess) return e;
-  fwd_sm100_kernel<D, kMode><<<grid, kThreads, L::kAlloc, stream>>>(tmQ, tmK, tmV, tmO, a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_early(fwd_sm100_kernel<D, kMode>, dim3(grid), kThreads, L::kAlloc, stream,
+                   kMode != kModNone && p.trace == nullptr, tmQ, tmK, tmV, tmO, a);
+  if (e != cudaSuccess) return e;
   return trace_mark(p, 1, stream);
 }
 

@@ -30,6 +30,36 @@ cudaError_t ready_kernel(Kernel* kernel, int regs, int smem, std::atomic<uint64_
   return cudaSuccess;
 }
 
+// Launch that may begin while the stream's previous kernel ends (programmatic dependent
+// launch, `early`): the kernel must execute grid_dependency_wait() before it touches memory
+// that an earlier kernel of the stream reads or writes, in every block, on every path.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem,
+                         cudaStream_t stream, bool early, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+#ifdef __CUDACC__
+// The stream's earlier kernels have ended and their writes are visible.
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// The stream's next kernel may be launched (it waits for this one's end by itself).
+__device__ __forceinline__ void grid_dependents_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+#endif
+
 // Problem shared by every kernel: [B*H, N, d] query-side tensors (Q, O, dO, dQ, LSE)
 // and [B*H, Nk, d] key-side tensors (K, V, dK, dV), contiguous.  Nk == N except for
 // the Nq != Nk entry points, whose queries are the last N of the Nk tokens.

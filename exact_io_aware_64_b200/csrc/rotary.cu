@@ -122,6 +122,7 @@ __device__ __forceinline__ void put16(void* p, uint4 v) {
 
 template <typename T, bool kInterleaved, bool kStream>
 __global__ void __launch_bounds__(kThreads) rotary_vector_kernel(const RotaryArgs a) {
+  grid_dependency_wait();
   const long long t0 = static_cast<long long>(blockIdx.x) * a.tokens;
   constexpr int kV = Vec<T>::n;
   constexpr int kAngles = kInterleaved ? kV / 2 : kV;
@@ -195,6 +196,7 @@ __global__ void __launch_bounds__(kThreads) rotary_vector_kernel(const RotaryArg
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) rotary_scalar_kernel(const RotaryArgs a) {
   extern __shared__ __align__(16) float2 cs[];
+  grid_dependency_wait();
   const int half = a.R / 2;
   const long long t0 = static_cast<long long>(blockIdx.x) * a.tokens;
   const int n = static_cast<int>(min(static_cast<long long>(a.tokens), a.total - t0));
@@ -260,8 +262,7 @@ cudaError_t launch_t(const RotaryArgs& args, bool vector, int num_sms, cudaStrea
       !vector ? (a.interleaved ? rotary_scalar_kernel<T, true> : rotary_scalar_kernel<T, false>)
       : stream_out ? (a.interleaved ? rotary_vector_kernel<T, true, true> : rotary_vector_kernel<T, false, true>)
                    : (a.interleaved ? rotary_vector_kernel<T, true, false> : rotary_vector_kernel<T, false, false>);
-  kernel<<<grid, kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_early(kernel, grid, kThreads, smem, stream, true, a);
 }
 
 }  // namespace

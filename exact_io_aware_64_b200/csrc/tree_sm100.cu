@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
+  grid_dependency_wait();
   // tile counts, then their prefix sums (warp 0)
   for (int b = threadIdx.x; b < a.B; b += kThreads) {
     int len, n;
@@ -211,8 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int end = min(total, begin + share);
   if (blockIdx.x == 0)  // the joining kernel reads the line's layout from here
     for (int b = threadIdx.x; b <= a.B; b += kThreads) a.prefix_out[b] = prefix[b];
-  // the joining kernel may be launched: it waits for this one's end by itself
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_dependents_launch();  // the joining kernel
   const uint32_t tmem = *tmem_slot;
   const uint32_t tS[2] = {tmem, tmem + 128};
   const uint32_t tO[2] = {tmem + 256, tmem + 256 + D};
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int r = static_cast<int>(out_row % a.rows);
   const int bh = static_cast<int>(out_row / a.rows);
   const int b = bh / a.Hkv, head = bh % a.Hkv;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_dependency_wait();
   const int n = a.seqlens_q != nullptr ? a.seqlens_q[b] : a.T;
   const int len = a.cache_lens[b];
   const int before = a.prefix_out[b], after = a.prefix_out[b + 1], total = a.prefix_out[a.B];
@@ -743,21 +743,14 @@ cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   KernelArgs ka;
   static_cast<TreeArgs&>(ka) = a;
   ka.cap = cap_args(a.scale, a.softcap);
-  kernel<<<num_sms, kThreads, Layout<D>::bytes(a.B), stream>>>(tmQ, tmK, tmV, ka);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_early(kernel, dim3(num_sms), kThreads, Layout<D>::bytes(a.B), stream, true, tmQ, tmK,
+                   tmV, ka);
+  if (e != cudaSuccess) return e;
   const long long rows = static_cast<long long>(a.B) * a.Hkv * a.rows;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows));
   const int threads = rows < kManyRows ? 256 : 64;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, threads == 256 ? tree_join_kernel<D, 256> : tree_join_kernel<D, 64>,
-                            a, static_cast<__nv_bfloat16*>(O), LSE, num_sms, kCopies);
+  return launch_early(threads == 256 ? tree_join_kernel<D, 256> : tree_join_kernel<D, 64>,
+                      dim3(static_cast<unsigned>(rows)), threads, 0, stream, true, a,
+                      static_cast<__nv_bfloat16*>(O), LSE, num_sms, kCopies);
 }
 
 }  // namespace
