@@ -583,7 +583,7 @@ def fwd_mod(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: Optional[f
     elif want_lse:
         LSE = Q.new_empty((B, H, Nq), dtype=torch.float32)
     _run("fa_fwd_mod", index, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
-         _ptr(LSE), *mods, B, H, Hkv, Nq, Nk, d, scale, int(bool(causal)), softcap)
+         _ptr(LSE), *mods, B, H, Hkv, Nq, Nk, d, float(scale), int(bool(causal)), float(softcap))
     return O, LSE
 
 
@@ -615,7 +615,8 @@ def bwd_mod(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tensor,
     ws_bytes = _check_workspace(workspace, index)
     _run("fa_bwd_mod", index, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
          dO.data_ptr(), LSE.data_ptr(), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), *mods, B, H,
-         Hkv, Nq, Nk, d, scale, int(bool(causal)), softcap, workspace.data_ptr(), ws_bytes)
+         Hkv, Nq, Nk, d, float(scale), int(bool(causal)), float(softcap), workspace.data_ptr(),
+         ws_bytes)
     return dQ, dK, dV
 
 
@@ -713,8 +714,8 @@ def _rotary(Q, K, inv_freq, positions, first, interleaved, mscale, Q_out, K_out,
         if not _like(positions, shape, torch.int32, index):
             _check_like("positions", positions, shape, torch.int32, index)
     _run("fa_rotary" if dtype is torch.bfloat16 else "fa_rotary_f32", index, Q.data_ptr(),
-         Q_out.data_ptr(), _ptr(K), _ptr(K_out), inv_freq.data_ptr(), _ptr(positions), first, B, H,
-         Hkv, N, d, 2 * half, int(bool(interleaved)), inverse, mscale, qs, ks)
+         Q_out.data_ptr(), _ptr(K), _ptr(K_out), inv_freq.data_ptr(), _ptr(positions), int(first), B, H,
+         Hkv, N, d, 2 * half, int(bool(interleaved)), inverse, float(mscale), qs, ks)
     return Q_out, K_out
 
 
@@ -805,8 +806,8 @@ def fwd_tree(Q: torch.Tensor, K_cache: torch.Tensor, V_cache: torch.Tensor,
     ws_bytes = _check_workspace(workspace, index)
     _run("fa_fwd_tree", index, Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(),
          O.data_ptr(), _ptr(LSE), block_table.data_ptr(), cache_lens.data_ptr(), _ptr(seqlens_q),
-         _ptr(tree_mask), B, H, Hkv, T, num_pages, page, max_pages, d, scale, softcap,
-         workspace.data_ptr(), ws_bytes)
+         _ptr(tree_mask), B, H, Hkv, T, num_pages, page, max_pages, d, float(scale),
+         float(softcap), workspace.data_ptr(), ws_bytes)
     return O, LSE
 
 

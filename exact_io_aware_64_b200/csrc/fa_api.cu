@@ -559,8 +559,11 @@ fa_status bwd_mod_impl(const void* Q, const void* K, const void* V, const void* 
 // One tensor of heads of a rotary call.  strides: {in b, h, n, out b, h, n} in elements, or
 // null for contiguous [B,heads,N,d] on both sides.
 fa_status rotary_tensor(const char* name, const void* in, void* out, int heads, int B, int N,
-                        int d, const long long* strides, int elem, fa::RotaryTensor* x) {
+                        int d, const long long* strides, int elem, fa::RotaryTensor* x,
+                        size_t extent[2], bool* in_place) {
   *x = fa::RotaryTensor{};
+  extent[0] = extent[1] = 0;
+  *in_place = true;
   if (heads < 0) return fail(FA_ERR_INVALID_ARG, "%s has %d heads", name, heads);
   if (heads == 0) return FA_OK;
   if (static_cast<long long>(heads) * N > 0x7fffffffll / B)
@@ -572,7 +575,6 @@ fa_status rotary_tensor(const char* name, const void* in, void* out, int heads, 
   const long long dense_n = d, dense_h = dense_n * N, dense_b = dense_h * heads;
   const long long dense[6] = {dense_b, dense_h, dense_n, dense_b, dense_h, dense_n};
   const long long* s = strides != nullptr ? strides : dense;
-  size_t extent[2];
   for (int o = 0; o < 2; ++o) {
     const long long n[3] = {B, heads, N};
     long long last = d;
@@ -589,8 +591,8 @@ fa_status rotary_tensor(const char* name, const void* in, void* out, int heads, 
     }
     extent[o] = static_cast<size_t>(last) * elem;
   }
-  const bool in_place = in == out && s[0] == s[3] && s[1] == s[4] && s[2] == s[5];
-  if (!in_place && overlaps(in, extent[0], out, extent[1]))
+  *in_place = in == out && s[0] == s[3] && s[1] == s[4] && s[2] == s[5];
+  if (!*in_place && overlaps(in, extent[0], out, extent[1]))
     return fail(FA_ERR_INVALID_ARG, "%s overlaps its output and is not the same tensor", name);
   *x = fa::RotaryTensor{in, out, heads, s[0], s[1], s[2], s[3], s[4], s[5]};
   return FA_OK;
@@ -617,11 +619,18 @@ fa_status rotary_impl(const void* Q, void* Q_out, const void* K, void* K_out,
                 static_cast<long long>(B) * N);
   if (B == 0 || N == 0) return FA_OK;
   fa::RotaryArgs a{};
-  FA_TRY(rotary_tensor("Q", Q, Q_out, H, B, N, d, q_strides, elem, &a.x[0]));
-  FA_TRY(rotary_tensor("K", K, K_out, Hkv, B, N, d, k_strides, elem, &a.x[1]));
+  size_t qx[2], kx[2];
+  bool q_in_place, k_in_place;
+  FA_TRY(rotary_tensor("Q", Q, Q_out, H, B, N, d, q_strides, elem, &a.x[0], qx, &q_in_place));
+  FA_TRY(rotary_tensor("K", K, K_out, Hkv, B, N, d, k_strides, elem, &a.x[1], kx, &k_in_place));
   if (H == 0 && Hkv == 0) return FA_OK;
-  if (H > 0 && Hkv > 0 && Q_out == K_out)
-    return fail(FA_ERR_INVALID_ARG, "Q and K have the same output");
+  if (H > 0 && Hkv > 0) {
+    if (Q_out == K_out) return fail(FA_ERR_INVALID_ARG, "Q and K have the same output");
+    // (heads of one fused buffer turned in place interleave, and so may two outputs)
+    if ((!q_in_place && overlaps(Q_out, qx[1], K, kx[0])) ||
+        (!k_in_place && overlaps(K_out, kx[1], Q, qx[0])))
+      return fail(FA_ERR_INVALID_ARG, "an output overlaps the other input");
+  }
   if (R > 0 && inv_freq == nullptr) return fail(FA_ERR_INVALID_ARG, "inv_freq is NULL");
   if (!aligned4(inv_freq) || !aligned4(positions))
     return fail(FA_ERR_INVALID_ARG, "inv_freq and positions must be 4-byte aligned");

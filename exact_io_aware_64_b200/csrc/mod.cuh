@@ -51,7 +51,8 @@ struct CapArgs {
   float in;        // scale / cap
   float out;       // cap log2(e)
   float neg_inv_out2;  // -1 / out^2
-  float top;       // |s| up to which q and g hold
+  float top;       // |s| up to which the tiles' usual path goes (see cap_args)
+  float poly;      // |s| up to which q holds; top <= poly
   float q[4];      // x = s q(s^2)
   float g[3];      // 1 - tanh^2 = g(s^2), for the backward pass
 };
@@ -59,11 +60,15 @@ struct CapArgs {
 // |y| <= 1/2: tanh(sqrt(u)) / sqrt(u) to degree 3, relative error 5.9e-7 evaluated in
 // float32, and sech^2(sqrt(u)) to degree 2, 1.6e-4 (it multiplies dS, which is rounded to
 // bf16 next, 2^-8).  Minimax in the relative error, fitted here by iteratively reweighted
-// least squares.
+// least squares.  Caps far above the scores use no more than |y| <= 1/5, where the Taylor
+// series of the same degrees are off by 5.6e-8 and 6e-4 y^2 at most: scores in the hundreds
+// then keep float32's digits.
 inline CapArgs cap_args(float scale, float softcap) {
-  const double p[4] = {0.9999994557706547, -0.33326317933916044, 0.13190296581699465,
-                       -0.04440222555557586};
-  const double d[3] = {0.9998382199693817, -0.9886407641960892, 0.5423509665406153};
+  const double minimax_p[4] = {0.9999994557706547, -0.33326317933916044, 0.13190296581699465,
+                               -0.04440222555557586};
+  const double minimax_d[3] = {0.9998382199693817, -0.9886407641960892, 0.5423509665406153};
+  const double taylor_p[4] = {1.0, -1.0 / 3, 2.0 / 15, -17.0 / 315};
+  const double taylor_d[3] = {1.0, -1.0, 2.0 / 3};
   CapArgs c{};
   if (softcap <= 0.f) return c;
   const double in = static_cast<double>(scale) / softcap;
@@ -77,6 +82,10 @@ inline CapArgs cap_args(float scale, float softcap) {
   double y = 0.5;
   if (out * std::tanh(y) > 50.0) y = std::atanh(50.0 / out);
   c.top = static_cast<float>(y / in);
+  const bool taylor = y < 0.2;
+  const double* p = taylor ? taylor_p : minimax_p;
+  const double* d = taylor ? taylor_d : minimax_d;
+  c.poly = static_cast<float>((taylor ? 0.2 : 0.5) / in);
   double f = 1.0;
   for (int i = 0; i < 4; ++i, f *= in * in) {
     c.q[i] = static_cast<float>(p[i] * f * out * in);
@@ -198,7 +207,7 @@ __device__ __forceinline__ float abs_max(const float* s) {
                      fmaxf(a8[6], a8[7]));
 }
 
-// Whether some |s| of the warp is past the polynomials' range (or not a number).
+// Whether some |s| of the warp is past the usual path's range (or not a number).
 __device__ __forceinline__ bool cap_over(float amax, const CapArgs& c) {
   return __any_sync(0xffffffffu, !(amax <= c.top));
 }
@@ -220,11 +229,12 @@ __device__ __forceinline__ float cap_tanh(float s, const CapArgs& c) {
 }
 
 // The capped score in log2 units of any raw product: the polynomial where it holds (its
-// error is relative), the formula beyond.
+// error is relative: a cap far above the scores must not cost them their digits), the
+// formula beyond.
 __device__ __forceinline__ float cap_any(float s, const CapArgs& c) {
   const float u = s * s;
   const float q = fmaf(u, fmaf(u, fmaf(u, c.q[3], c.q[2]), c.q[1]), c.q[0]);
-  return fabsf(s) <= c.top ? s * q : c.out * cap_tanh(s, c);
+  return fabsf(s) <= c.poly ? s * q : c.out * cap_tanh(s, c);
 }
 
 // N raw products to capped scores in place, by cap_any: for the tiles with a score past the

@@ -490,7 +490,9 @@ FA_API size_t fa_bwd_noalloc_max_scratch_bytes(void);
  * Kernel-boundary timing, for profilers.  While a list of events is set on the calling
  * thread, every forward and backward call records events[0] on its stream just before
  * its first kernel and events[k] just after its k-th kernel; the forward calls launch
- * one kernel, the backward calls three (D preparation, dK/dV, dQ).  Boundaries
+ * one kernel, the backward calls three (D preparation, dK/dV, dQ); fa_doc_ranges,
+ * fa_rotary and fa_fwd_tree record nothing.  (Traced _mod calls run their kernels one after
+ * the other; otherwise dQ may begin on SMs that dK/dV has left.)  Boundaries
  * beyond n - 1 are not recorded.  The events are caller-created cudaEvent_t (timing
  * enabled) and stay caller-owned.  fa_trace_events(NULL, 0) stops recording.
  * Returns FA_ERR_INVALID_ARG if n < 0, n > 8, or events is NULL with n > 0.

@@ -142,6 +142,12 @@ def test_softcap_range(softcap):
           exact=softcap > 0.1)
 
 
+@pytest.mark.parametrize("softcap", [200.0, 1e4, 1e6, 1e8])
+def test_scores_above_a_hundred_under_a_large_cap(softcap):
+    """A cap far above the scores changes little and must not cost them their digits."""
+    check(1, 1, 1, 300, 300, 64, causal=True, softcap=softcap, seed=12, sigma=6.0, exact=False)
+
+
 def test_softcap_saturates():
     """Scores far past the cap: every tanh is +-1 and the derivative vanishes."""
     check(1, 1, 1, 200, 200, 64, softcap=2.0, seed=4, sigma=20.0, exact=False)
@@ -216,6 +222,81 @@ def test_unmodified_matches_the_plain_calls(d):
         for a, b in zip(binding.bwd(q, k, v, O, do, L, causal=causal),
                         binding.bwd_mod(q, k, v, O, do, L, causal=causal)):
             assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace and outputs, overlap freely."""
+    sets = []
+    for seed in (1, 2):
+        ins = make(2, 4, 2, 900, 900, 128, seed)
+        q, k, v, do = (ins[n].cuda() for n in ("Q", "K", "V", "dO"))
+        kw = {"causal": True, "softcap": 20.0, "docs": binding.doc_ranges(doc_ids(2, 900, 200, seed).cuda())}
+        O, L = binding.fwd_mod(q, k, v, **kw)
+        sets.append((q, k, v, do, kw, [O, L, *binding.bwd_mod(q, k, v, O, do, L, **kw)],
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(10):
+        for i, (q, k, v, do, kw, _, s) in enumerate(sets):
+            O, L = binding.fwd_mod(q, k, v, stream=s, **kw)
+            got[i] = [O, L, *binding.bwd_mod(q, k, v, O, do, L, stream=s, **kw)]
+    torch.cuda.synchronize()
+    binding.check_device_error()
+    for g, s in zip(got, sets):
+        assert all(torch.equal(a, b) for a, b in zip(g, s[5]))
+
+
+def test_after_other_work_of_the_stream():
+    """The kernels may be launched before the stream's earlier work ends; they must not read
+    their inputs, or write outputs that it still reads, before it has.  Eager and captured."""
+    B, H, N, d = 1, 8, 1500, 128
+    ins = make(B, H, H, N, N, d, 9)
+    src = [ins[n].cuda() for n in ("Q", "K", "V", "dO")]
+    ids = doc_ids(B, N, 300, 2).cuda()
+    bufs = [torch.empty_like(t) for t in src]
+    idb = torch.empty_like(ids)
+    O, L = torch.empty_like(src[0]), torch.empty((B, H, N), device="cuda")
+    grads = [torch.empty_like(t) for t in src[:3]]
+    keep = [torch.empty_like(t) for t in (O, *grads)]
+    ws = torch.empty(binding.workspace_bytes(B, H, N, d), dtype=torch.uint8, device="cuda")
+    rng = [torch.empty_like(ids), torch.empty_like(ids)]
+
+    def step():
+        for b, s in zip((*bufs, idb), (*src, ids)):
+            b.copy_(s)
+        docs = binding.doc_ranges(idb, *rng)
+        idb.fill_(-1)
+        binding.fwd_mod(*bufs[:3], causal=True, docs=docs, O=O, LSE=L)
+        binding.bwd_mod(*bufs[:3], O, bufs[3], L, causal=True, docs=docs, dQ=grads[0], dK=grads[1],
+                        dV=grads[2], workspace=ws)
+        for k, t in zip(keep, (O, *grads)):
+            k.copy_(t)
+        for t in (*bufs, O, L, *grads, *rng, ws):
+            t.fill_(1)
+
+    step()
+    torch.cuda.synchronize()
+    first = [t.clone() for t in keep]
+    docs = binding.doc_ranges(ids)
+    want, wl = binding.fwd_mod(*src[:3], causal=True, docs=docs)
+    torch.cuda.synchronize()
+    assert torch.equal(first[0], want)
+    for a, b in zip(first[1:], binding.bwd_mod(*src[:3], want, src[3], wl, causal=True, docs=docs)):
+        assert torch.equal(a, b)
+    for _ in range(20):
+        step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, keep))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, capture_error_mode="relaxed"):
+        step()
+    for t in keep:
+        t.zero_()
+    for _ in range(5):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, keep))
+    del g
 
 
 def test_in_a_cuda_graph_and_on_another_stream():

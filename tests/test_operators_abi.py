@@ -95,7 +95,7 @@ def test_rotary_refusals(fn):
            {"Qo": P[0] + 64}, {"Qo": P[3]}, {"B": 1 << 16, "N": 1 << 15}, {"first": 1 << 50},
            {"qs": strides(-1, 640, 64, 2560, 640, 64)}, {"qs": strides(2560, 640, 64, 2560, 640, 0)},
            {"qs": strides(1 << 41, 640, 64, 2560, 640, 64)},
-           {"H": 1 << 28, "N": 1 << 6}]
+           {"H": 1 << 28, "N": 1 << 6}, {"Qo": P[2] + 64}, {"Ko": P[0] + 64}, {"Qo": P[2]}]
     for kw in bad:
         st, msg = call(fn, *ROT, **kw)
         assert st == BAD and msg, kw

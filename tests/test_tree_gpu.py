@@ -96,7 +96,7 @@ def check(B, H, Hkv, T, lens, d, page, *, drafted=None, mask=True, softcap=0.0, 
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("page", [8, 16, 32, 64, 128, 256])
+@pytest.mark.parametrize("page", [8, 16, 32, 64, 128, 256, 384])
 @pytest.mark.parametrize("L", [1, 7, 64, 127, 128, 129, 1000])
 def test_one_token(L, page, d):
     check(1, 2, 2, 1, [L], d, page, mask=False, seed=L + page)
@@ -139,6 +139,31 @@ def test_softcap(softcap, d):
 def test_long_sequence_split_over_the_gpu():
     check(1, 2, 1, 1, [60000], 128, 64, mask=False, seed=12)
     check(2, 16, 2, 32, [20000, 300], 128, 128, seed=13, heads=(0, 7, 15))
+
+
+def test_long_tables_of_every_page_size():
+    """Tables longer than the 64 entries that the loading warp holds at once."""
+    for page in (8, 16, 64, 128, 384):
+        check(1, 2, 1, 3, [9000 + page], 64, page, seed=page)
+
+
+def test_cache_past_32_bits():
+    """Pages that begin more than 2^32 bytes (and 2^31 elements) into the cache."""
+    page, Hkv, d, L = 64, 8, 128, 500
+    num = (1 << 31) // (Hkv * page * d) + 40
+    K, V = (torch.empty(num, Hkv, page, d, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    n = -(-L // page)
+    ids = torch.arange(num - n, num, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for c in (K, V):
+        c[num - n:] = torch.randn(n, Hkv, page, d, generator=g, device="cuda").bfloat16()
+    q = torch.randn(1, 16, 1, d, generator=g, device="cuda").bfloat16()
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    O, LSE = binding.fwd_tree(q, K, V, ids[None].contiguous(), lens)
+    small = [c[num - n:].clone() for c in (K, V)]
+    want, wl = binding.fwd_tree(q, *small, (ids - (num - n))[None].contiguous(), lens)
+    binding.check_device_error()
+    assert torch.equal(O, want) and torch.equal(LSE, wl)
 
 
 def test_rows_that_see_nothing():
