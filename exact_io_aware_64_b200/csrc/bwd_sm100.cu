@@ -45,6 +45,13 @@
 // two halves as the two halves of each group's P^T(i) are written;
 //  dQ: S(j) dP(j) | S(j+1) dQ(j) dP(j+1) | S(j+2) dQ(j+1) dP(j+2) | ...).
 // Causal work units are ordered heaviest first.
+//
+// Modified scores (mod.cuh) are a template mode of kernels 2 and 3.  dK/dV units belong to a
+// key head and walk the query tiles of each of its query heads in turn, so shared heads'
+// gradients add up in the same float32 accumulators.  Without a modification the kernels
+// take the time of the unmodified ones; capped scores take B=1 H=16 N=8192 d=128 causal from
+// 826 us to 1030 (B=2 N=4096: 455 to 555), bound by the element-wise warps: two to a
+// scheduler, most of their stalls fixed-latency dependencies and instruction fetch.
 #include <cstdint>
 
 #include "internal.h"

@@ -52,6 +52,12 @@
 //     cu_k[b]); the tensor maps address (column, head, token), so a tile is 128 tokens of
 //     one head from the sequence's first token on.  Tile rows past the sequence hold the
 //     next sequence's tokens: masked as keys, not stored as queries.
+//   * Modified scores (mod.cuh): kMode compiles the kernel once per combination of cap and
+//     distance bias.  A unit walks the key tiles between its first row's first and its last
+//     row's last visible key, K and V come from the query head's key head, and units of
+//     documents are dealt dearest first.  A capped score costs 4 packed multiply-adds an
+//     entry: B=1 H=16 N=8192 d=128 causal 316 us against 264 without a cap (B=2 N=4096: 180
+//     against 147), bound, as without, by the softmax warps' instruction stream.
 #include <cfloat>
 #include <cstdint>
 
