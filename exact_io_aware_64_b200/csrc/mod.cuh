@@ -12,8 +12,8 @@
 // a key's queries are one interval of positions too,
 //       [max(start[j], causal and j >= prefix ? j : 0), end[j]),
 // and both ends of either rise with the row.  So the first and the last row of a tile
-// give the tiles it meets and the part that needs no element mask, and an element mask
-// costs one subtraction and one unsigned compare.  (Arrays of the caller's making that
+// give the tiles it meets and the part that needs no element mask, and where one is needed
+// 32 entries' visibility is one word of bits.  (Arrays of the caller's making that
 // do not rise give unspecified results, never an access out of range: every limit is
 // clamped to the sequence.)
 #pragma once
@@ -237,18 +237,26 @@ __device__ __forceinline__ float cap_any(float s, const CapArgs& c) {
   return fabsf(s) <= c.poly ? s * q : c.out * cap_tanh(s, c);
 }
 
-// N raw products to capped scores in place, by cap_any: for the tiles with a score past the
-// polynomial's range.  A rolled loop over a copy in local memory, so that what seldom runs
-// takes little of the instruction cache.
+// N raw products to capped scores in place, for the tiles with a score past the usual path's
+// range: the formula for all of them, in registers, while its absolute error, 2^-23 out, is
+// far below the rounding of P (out <= 256).  Larger caps go entry by entry through a copy in
+// local memory: a rolled loop, which leaves the instruction cache to the usual path, but
+// which the small L1 beside the kernels' shared memory makes several times slower than the
+// tile's other work.
 template <int N>
 __device__ __forceinline__ void cap_scores_any(float* s, const CapArgs& c) {
-  float t[N];
+  if (c.out <= 256.f) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) t[k] = s[k];
+    for (int k = 0; k < N; ++k) s[k] = c.out * cap_tanh(s[k], c);
+  } else {
+    float t[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) t[k] = s[k];
 #pragma unroll 1
-  for (int k = 0; k < N; ++k) t[k] = cap_any(t[k], c);
+    for (int k = 0; k < N; ++k) t[k] = cap_any(t[k], c);
 #pragma unroll
-  for (int k = 0; k < N; ++k) s[k] = t[k];
+    for (int k = 0; k < N; ++k) s[k] = t[k];
+  }
 }
 
 // The same by the polynomial.
