@@ -50,7 +50,7 @@
 // key head and walk the query tiles of each of its query heads in turn, so shared heads'
 // gradients add up in the same float32 accumulators.  Without a modification the kernels
 // take the time of the unmodified ones; capped scores take B=1 H=16 N=8192 d=128 causal from
-// 826 us to 1030 (B=2 N=4096: 455 to 555), bound by the element-wise warps: two to a
+// 806 us to 1002 (B=2 N=4096: 451 to 548), bound by the element-wise warps: two to a
 // scheduler, most of their stalls fixed-latency dependencies and instruction fetch.
 #include <cstdint>
 

@@ -55,9 +55,11 @@
 //   * Modified scores (mod.cuh): kMode compiles the kernel once per combination of cap and
 //     distance bias.  A unit walks the key tiles between its first row's first and its last
 //     row's last visible key, K and V come from the query head's key head, and units of
-//     documents are dealt dearest first.  A capped score costs 4 packed multiply-adds an
-//     entry: B=1 H=16 N=8192 d=128 causal 316 us against 264 without a cap (B=2 N=4096: 180
-//     against 147), bound, as without, by the softmax warps' instruction stream.
+//     documents are dealt dearest first.  A capped score costs 5 packed operations for two
+//     entries: B=1 H=16 N=8192 d=128 causal 332 us against 270 without a cap (B=2 N=4096: 187
+//     against 145), bound, as without, by the softmax warps' instruction stream.  Where every
+//     score is near its cap the formula's two exponential-unit operations an entry make it
+//     350 (B=2 N=4096).
 #include <cfloat>
 #include <cstdint>
 
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           partial = kv0 < full_lo || kv0 + kBN > full_hi;
           if constexpr (has_cap(kMode)) {
             amax = abs_max<kBN>(s);
-            const bool over = cap_over(amax, args.mod.cap);
+            const bool over = cap_over(amax, args.mod.cap.top);
             capped = !has_bias(kMode) && !over;
             if (seldom(over)) {
               cap_scores_any<kBN>(s, args.mod.cap);

@@ -51,24 +51,33 @@ struct CapArgs {
   float in;        // scale / cap
   float out;       // cap log2(e)
   float neg_inv_out2;  // -1 / out^2
-  float top;       // |s| up to which the tiles' usual path goes (see cap_args)
+  float top;       // |s| up to which the forward's usual path goes (see cap_args)
   float poly;      // |s| up to which q holds; top <= poly
-  float q[4];      // x = s q(s^2)
-  float g[3];      // 1 - tanh^2 = g(s^2), for the backward pass
+  float q[5];      // x = s q(s^2)
+  float top_b;     // |s| up to which the backward uses qb and g
+  float qb[4];     // x = s qb(s^2)
+  float g[3];      // 1 - tanh^2 = g(s^2)
 };
 
-// |y| <= 1/2: tanh(sqrt(u)) / sqrt(u) to degree 3, relative error 5.9e-7 evaluated in
-// float32, and sech^2(sqrt(u)) to degree 2, 1.6e-4 (it multiplies dS, which is rounded to
+// tanh(sqrt(u)) / sqrt(u) as polynomials: to degree 4 for |y| <= 0.8, relative error 1.1e-6
+// evaluated in float32, for the forward; to degree 3 for |y| <= 1/2, 5.9e-7, for the
+// backward, with sech^2(sqrt(u)) to degree 2, 1.6e-4 (it multiplies dS, which is rounded to
 // bf16 next, 2^-8).  Minimax in the relative error, fitted here by iteratively reweighted
-// least squares.  Caps far above the scores use no more than |y| <= 1/5, where the Taylor
-// series of the same degrees are off by 5.6e-8 and 6e-4 y^2 at most: scores in the hundreds
-// then keep float32's digits.
+// least squares.  The forward pays 6 % for its wider range (B=2 H=16 N=4096 d=128 causal, Q
+// and K of deviation 1.5, cap 50: 182 us against 171 with degree 3), because a tile outside
+// it costs the forward more: with 1/2, scores of that size under a cap of 20 took 318 us,
+// now 183.  The backward takes 560 us either way there and 4 % less under the larger cap.
+// Caps far above the scores use no more than |y| <= 1/5, where the Taylor series of the
+// same degrees are off by 5.6e-8 (degree 3; less for 4) and 6e-4 y^2 at most: scores in the
+// hundreds then keep float32's digits.
 inline CapArgs cap_args(float scale, float softcap) {
-  const double minimax_p[4] = {0.9999994557706547, -0.33326317933916044, 0.13190296581699465,
-                               -0.04440222555557586};
-  const double minimax_d[3] = {0.9998382199693817, -0.9886407641960892, 0.5423509665406153};
-  const double taylor_p[4] = {1.0, -1.0 / 3, 2.0 / 15, -17.0 / 315};
-  const double taylor_d[3] = {1.0, -1.0, 2.0 / 3};
+  const double fit_q[5] = {0.9999989943428248, -0.33325371953005856, 0.13230565487990226,
+                           -0.049180140355985856, 0.01210013750460391};
+  const double fit_qb[4] = {0.9999994557706547, -0.33326317933916044, 0.13190296581699465,
+                            -0.04440222555557586};
+  const double fit_g[3] = {0.9998382199693817, -0.9886407641960892, 0.5423509665406153};
+  const double taylor_q[5] = {1.0, -1.0 / 3, 2.0 / 15, -17.0 / 315, 62.0 / 2835};
+  const double taylor_g[3] = {1.0, -1.0, 2.0 / 3};
   CapArgs c{};
   if (softcap <= 0.f) return c;
   const double in = static_cast<double>(scale) / softcap;
@@ -78,18 +87,21 @@ inline CapArgs cap_args(float scale, float softcap) {
   c.neg_inv_out2 = static_cast<float>(-1.0 / (out * out));
   // The forward takes the score of a row's largest |s| for its reference maximum; scores
   // then lie within 2 * 50 of it, so the largest probability is at least 2^-100, far from
-  // float32's (and bf16's) smallest: out * tanh(y) <= 50 bounds y for caps above 75.
-  double y = 0.5;
+  // float32's (and bf16's) smallest: out * tanh(y) <= 50 bounds y for caps above 52.
+  double y = 0.8;
   if (out * std::tanh(y) > 50.0) y = std::atanh(50.0 / out);
-  c.top = static_cast<float>(y / in);
   const bool taylor = y < 0.2;
-  const double* p = taylor ? taylor_p : minimax_p;
-  const double* d = taylor ? taylor_d : minimax_d;
-  c.poly = static_cast<float>((taylor ? 0.2 : 0.5) / in);
+  c.top = static_cast<float>(y / in);
+  c.poly = static_cast<float>((taylor ? 0.2 : 0.8) / in);
+  c.top_b = static_cast<float>((taylor ? 0.2 : 0.5) / in);
+  const double* q = taylor ? taylor_q : fit_q;
+  const double* qb = taylor ? taylor_q : fit_qb;
+  const double* g = taylor ? taylor_g : fit_g;
   double f = 1.0;
-  for (int i = 0; i < 4; ++i, f *= in * in) {
-    c.q[i] = static_cast<float>(p[i] * f * out * in);
-    if (i < 3) c.g[i] = static_cast<float>(d[i] * f);
+  for (int i = 0; i < 5; ++i, f *= in * in) {
+    c.q[i] = static_cast<float>(q[i] * f * out * in);
+    if (i < 4) c.qb[i] = static_cast<float>(qb[i] * f * out * in);
+    if (i < 3) c.g[i] = static_cast<float>(g[i] * f);
   }
   return c;
 }
@@ -208,15 +220,16 @@ __device__ __forceinline__ float abs_max(const float* s) {
 }
 
 // Whether some |s| of the warp is past the usual path's range (or not a number).
-__device__ __forceinline__ bool cap_over(float amax, const CapArgs& c) {
-  return __any_sync(0xffffffffu, !(amax <= c.top));
+__device__ __forceinline__ bool cap_over(float amax, float top) {
+  return __any_sync(0xffffffffu, !(amax <= top));
 }
 
 // q(s^2) of a pair: the factor that takes s to its capped score in log2 units.
 __device__ __forceinline__ uint64_t cap_factor(uint64_t s2, const CapArgs& c) {
   using namespace sm100;
   const uint64_t u = mul_x2(s2, s2);
-  uint64_t q = fma_x2(u, f32x2(c.q[3], c.q[3]), f32x2(c.q[2], c.q[2]));
+  uint64_t q = fma_x2(u, f32x2(c.q[4], c.q[4]), f32x2(c.q[3], c.q[3]));
+  q = fma_x2(u, q, f32x2(c.q[2], c.q[2]));
   q = fma_x2(u, q, f32x2(c.q[1], c.q[1]));
   return fma_x2(u, q, f32x2(c.q[0], c.q[0]));
 }
@@ -233,7 +246,7 @@ __device__ __forceinline__ float cap_tanh(float s, const CapArgs& c) {
 // formula beyond.
 __device__ __forceinline__ float cap_any(float s, const CapArgs& c) {
   const float u = s * s;
-  const float q = fmaf(u, fmaf(u, fmaf(u, c.q[3], c.q[2]), c.q[1]), c.q[0]);
+  const float q = fmaf(u, fmaf(u, fmaf(u, fmaf(u, c.q[4], c.q[3]), c.q[2]), c.q[1]), c.q[0]);
   return fabsf(s) <= c.poly ? s * q : c.out * cap_tanh(s, c);
 }
 
@@ -306,8 +319,8 @@ __device__ __forceinline__ bool mod_probs(float* s, float* p, uint32_t* pk, cons
   bool over = false;
   float q0 = 0.f, q1 = 0.f, q2 = 0.f, q3 = 0.f;
   if constexpr (has_cap(kMode)) {
-    q0 = m.cap.q[0], q1 = m.cap.q[1], q2 = m.cap.q[2], q3 = m.cap.q[3];
-    over = cap_over(abs_max<N>(s), m.cap);
+    q0 = m.cap.qb[0], q1 = m.cap.qb[1], q2 = m.cap.qb[2], q3 = m.cap.qb[3];
+    over = cap_over(abs_max<N>(s), m.cap.top_b);
     if (seldom(over)) {
       cap_scores_any<N>(s, m.cap);
       q0 = 1.f, q1 = q2 = q3 = 0.f;

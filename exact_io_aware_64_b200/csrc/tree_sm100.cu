@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kCap) {
           hide(0.f);  // (what lies behind the end does not choose the form)
           amax = abs_max<kCols>(s);
-          const bool over = cap_over(amax, a.cap);
+          const bool over = cap_over(amax, a.cap.top);
           capped = !tail && !over;
           if (!capped) {
             if (seldom(over))
