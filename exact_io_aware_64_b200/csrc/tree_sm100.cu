@@ -13,9 +13,9 @@
 //
 // Measured: 32 sequences of 8192 tokens, 16 heads over 4, d = 128: 94 us, 87 % of the copy
 // rate with both kernels and their launches (64 sequences: 173 us, 95 %); d = 64, 64
-// sequences: 103 us, 80 %, bound by the chain of products, softmax and barriers of a tile
+// sequences: 101 us, 81 %, bound by the chain of products, softmax and barriers of a tile
 // half the size.  256 rows a key head (32 drafted tokens x 8 heads), 8 x 32768 tokens: 85 us,
-// 99 capped, against 41 for the bytes: the softmax of two full row tiles, 2.8 us a key tile,
+// 104 capped, against 41 for the bytes: the softmax of two full row tiles, 2.8 us a key tile,
 // paces it as it does the forward kernel.
 //
 // Split: the key tiles of all (sequence, key head, row tile pair) segments form one line
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t issued_phase[L::kStages];
     for (int s = 0; s < L::kStages; ++s) issued[s] = 0, issued_phase[s] = 0;
     // This warp paces short tiles (with divisions and a table read per load it took 2060
-    // cycles a tile, which held a d = 64 batch of 64 x 8192 tokens to 135 us; 103 as it is),
+    // cycles a tile, which held a d = 64 batch of 64 x 8192 tokens to 135 us; 101 as it is),
     // so it divides and reads the table seldom.  Pages below 128
     // tokens are a power of two: a tile is `per` boxes of a page each, lane p fetching box p;
     // larger pages hold `tiles` tiles of one box each.
