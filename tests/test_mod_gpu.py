@@ -224,6 +224,18 @@ def test_unmodified_matches_the_plain_calls(d):
             assert torch.equal(a, b)
 
 
+def test_keys_without_queries():
+    """Nq = 0: no query sees any key, so dK and dV of every key head are zero."""
+    q = torch.empty(2, 6, 0, 64, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.randn(2, 3, 50, 64, device="cuda").bfloat16() for _ in "kv")
+    O, L = binding.fwd_mod(q, k, v, causal=True, softcap=10.0)
+    assert O.shape == q.shape and L.shape == (2, 6, 0)
+    dK, dV = torch.full_like(k, 7.0), torch.full_like(v, 7.0)
+    dQ, _, _ = binding.bwd_mod(q, k, v, O, q, L, causal=True, softcap=10.0, dK=dK, dV=dV)
+    binding.check_device_error()
+    assert dQ.shape == q.shape and not dK.any() and not dV.any()
+
+
 def test_two_streams_at_once():
     """Calls on two streams, each with its own workspace and outputs, overlap freely."""
     sets = []

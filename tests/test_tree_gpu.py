@@ -166,6 +166,27 @@ def test_cache_past_32_bits():
     assert torch.equal(O, want) and torch.equal(LSE, wl)
 
 
+def test_outputs_made_on_a_given_stream():
+    """With fewer drafted tokens than rows and no outputs given, the rows behind them are
+    zeros and -inf, filled on the stream that the kernels run on."""
+    Q, K, V, table = build(3, 4, 2, 8, [90, 60, 8], 128, 16, 21)
+    args = (Q.cuda(), K.cuda(), V.cuda(), table.cuda(),
+            torch.tensor([90, 60, 8], dtype=torch.int32).cuda())
+    n = torch.tensor([8, 0, 3], dtype=torch.int32).cuda()
+    want, wl = binding.fwd_tree(*args, seqlens_q=n)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        O, L = binding.fwd_tree(*args, seqlens_q=n, stream=side)
+    side.synchronize()
+    binding.check_device_error()
+    assert torch.equal(O, want) and torch.equal(L, wl)
+    assert not O[1].any() and not O[2, :, 3:].any()
+    assert torch.isneginf(L[1]).all() and torch.isneginf(L[2, :, 3:]).all()
+    assert torch.isfinite(L[0]).all() and torch.isfinite(L[2, :, :3]).all()
+
+
 def test_rows_that_see_nothing():
     """A sequence that is all draft, and masks with no bit: O = 0, LSE = -inf."""
     Q, K, V, table = build(1, 2, 1, 4, [4], 64, 16, 5)
