@@ -667,8 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               d2 = add_x2(d2, two2);
             }
           }
-          // hidden entries: -inf, or (capped) probability 0 below -- their products are
-          // ordinary scores, which the reference maximum may take in
+          // hidden entries: -inf, or (capped) probability 0 below -- where the row sees a key
+          // of the tile, the reference maximum may take their products in
           if (partial && !capped) {
 #pragma unroll
             for (int q = 0; q < kBN / 32; ++q) {
@@ -695,8 +695,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m_tile;
         if (has_cap(kMode) && capped) {
           // the cap rises, so no score of the row is above that of its largest |s|, which
-          // serves as the reference as well as the largest score would (see cap_args)
+          // serves as the reference as well as the largest score would (see cap_args), if
+          // the row sees a key of this tile: one that it walks for other rows sets nothing
           m_tile = args.mod.cap.out * cap_tanh(amax, args.mod.cap);
+          if (max(lim_row.lo, kv0) >= min(lim_row.hi, kv0 + kBN)) m_tile = -INFINITY;
         } else {
           float mx8[8];
 #pragma unroll

@@ -85,9 +85,11 @@ inline CapArgs cap_args(float scale, float softcap) {
   c.in = static_cast<float>(in);
   c.out = static_cast<float>(out);
   c.neg_inv_out2 = static_cast<float>(-1.0 / (out * out));
-  // The forward takes the score of a row's largest |s| for its reference maximum; scores
-  // then lie within 2 * 50 of it, so the largest probability is at least 2^-100, far from
-  // float32's (and bf16's) smallest: out * tanh(y) <= 50 bounds y for caps above 52.
+  // In a tile of which a row sees a key, the forward takes the score of the largest |s| for
+  // the row's reference maximum.  The visible one is then within 2 * 50 of it, so the largest
+  // probability of the row is at least 2^-100, far from float32's (and bf16's) smallest: out *
+  // tanh(y) <= 50 bounds y for caps above 52.  (A tile that the row sees nothing of must not
+  // set its reference: the visible scores may all lie past the range, down to -out.)
   double y = 0.8;
   if (out * std::tanh(y) > 50.0) y = std::atanh(50.0 / out);
   const bool taylor = y < 0.2;

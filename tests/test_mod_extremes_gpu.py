@@ -1,0 +1,147 @@
+"""Modified-score attention (fa_fwd_mod, fa_bwd_mod) where hidden and visible scores lie far
+apart, against the float64 definition, head by head.
+
+Tolerances, element by element, half a step of bf16 being 2^-8 of a value.  A float32 score x
+is off by 1.1e-6 |x| where the cap is the polynomial, by 2^-22 cap where it is the formula
+(below 4.3e-5 for caps up to 177, which use it for whole tiles; below 2^-19 |x| for larger
+ones, which use it above a fifth of the cap), and by 2^-21 |x| for the product, the scale, the
+subtraction of the maximum and the logarithm: by 2^-19 |x| + 4.3e-5.  LSE may be off by 2^-19
+|x| + 1e-4, a probability by
+  eP = P (2^-8 + 2^-18 |x| + 1e-4)
+(its rounding, its score and LSE or sum, the exponential), dP - D by 2^-20 of the products that
+make it (d and Nk of them in float32, whose roundings add up like their root), and
+  eS = |dS| (2^-8 + 2^-18 |x| + 3e-4) + P dz 2^-20 (|dO| |V|^T + |dO| . |O|)
+(3e-4: the cap's derivative, 1.6e-4, beside eP's).  Then O, dV, dQ and dK are off by
+eP |V|, eP^T |dO|, scale eS |K| and scale eS^T |Q| and by their own rounding.  These bounds do
+not presume scores of any size: where all of a row's keys share a large column, its dQ there
+is a difference of large products, each rounded.  The gradients are compared with the
+formula's from the O that the call is handed.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mod_reference as ref
+from exact_io_aware_64_b200 import binding
+from parity import to64
+
+pytestmark = pytest.mark.gpu
+
+
+HALF = 2.0 ** -8
+
+
+def assert_within(got, want, bound, what):
+    over = np.abs(got - want) - (bound + HALF * np.abs(want) + 1e-30)
+    assert over.max(initial=0.0) <= 0, f"{what}: {over.max():.3e} over its bound"
+
+
+def check(q, k, v, do, *, causal=False, softcap=0.0, slopes=None, prefix=None, ids=None,
+          heads=None, sequences=None):
+    """Forward and backward of bf16 CPU tensors against float64, for the given query heads'
+    O, LSE and dQ and, where all the heads of a key head are given, its dK and dV."""
+    B, H, Nq, d = q.shape
+    Hkv, Nk = k.shape[1:3]
+    scale = d ** -0.5
+    kw = {"causal": causal, "softcap": softcap,
+          "slopes": None if slopes is None else torch.tensor(slopes, dtype=torch.float32).cuda(),
+          "prefix": None if prefix is None else torch.tensor(prefix, dtype=torch.int32).cuda(),
+          "docs": None if ids is None else binding.doc_ranges(ids.cuda())}
+    gpu = [t.cuda() for t in (q, k, v)]
+    O = torch.full_like(gpu[0], float("nan"))
+    LSE = torch.full((B, H, Nq), float("nan"), device="cuda")
+    binding.fwd_mod(*gpu, O=O, LSE=LSE, **kw)
+    grads = [torch.full_like(t, float("nan")) for t in gpu]
+    binding.bwd_mod(*gpu, O, do.cuda(), LSE, dQ=grads[0], dK=grads[1], dV=grads[2], **kw)
+    binding.check_device_error()
+    assert all(torch.isfinite(t).all() for t in (O, *grads))
+    heads = range(H) if heads is None else heads
+    for b in range(B) if sequences is None else sequences:
+        seen = ref.visible(Nq, Nk, causal, None if prefix is None else prefix[b],
+                           None if ids is None else ids[b].numpy())
+        empty, blind = ~seen.any(axis=1), ~seen.any(axis=0)
+        sums, n = {}, {}
+        for h in heads:
+            c = h // (H // Hkv)
+            Qh, Kh, Vh, Gh = (to64(t) for t in (q[b, h], k[b, c], v[b, c], do[b, h]))
+            sl = None if slopes is None else float(np.float32(slopes[h]))
+            rO, rL, P = ref.forward(Qh, Kh, Vh, scale, seen, softcap, sl)
+            x, dz = ref.scores(Qh, Kh, scale, softcap, sl)
+            gO, gL = to64(O[b, h]), to64(LSE[b, h])
+            assert (gO[empty] == 0).all() and np.isneginf(gL[empty]).all()
+            ax = np.where(seen, np.abs(x), 0.0).max(axis=1, keepdims=True)
+            off = np.abs(gL - rL)[~empty] - (1e-4 + 2.0 ** -19 * ax[~empty, 0])
+            assert off.max(initial=0.0) <= 0, f"LSE b={b} h={h}: {off.max():.3e} over its bound"
+            eP = P * (HALF + 2.0 ** -18 * ax + 1e-4)
+            assert_within(gO, rO, eP @ np.abs(Vh), f"O b={b} h={h}")
+            dQ, dK, dV = ref.backward(Qh, Kh, Vh, Gh, scale, seen, softcap, sl, O=gO)
+            D = (Gh * gO).sum(axis=1, keepdims=True)
+            eS = (np.abs(P * (Gh @ Vh.T - D) * dz) * (HALF + 2.0 ** -18 * ax + 3e-4) +
+                  P * dz * 2.0 ** -20 * (np.abs(Gh) @ np.abs(Vh).T +
+                                         (np.abs(Gh) * np.abs(gO)).sum(axis=1, keepdims=True)))
+            g = to64(grads[0][b, h])
+            assert (g[empty] == 0).all()
+            assert_within(g, dQ, scale * eS @ np.abs(Kh), f"dQ b={b} h={h}")
+            mine = (dK, scale * eS.T @ np.abs(Qh), dV, eP.T @ np.abs(Gh))
+            sums[c] = [s + t for s, t in zip(sums.get(c, (0.0,) * 4), mine)]
+            n[c] = n.get(c, 0) + 1
+        for c, (dK, eK, dV, eV) in sums.items():
+            gk, gv = to64(grads[1][b, c]), to64(grads[2][b, c])
+            assert (gk[blind] == 0).all() and (gv[blind] == 0).all()
+            if n[c] == H // Hkv:
+                assert_within(gk, dK, eK, f"dK b={b} head {c}")
+                assert_within(gv, dV, eV, f"dV b={b} head {c}")
+
+
+# ------------------------------------------------------------------ scores of given size
+def placed(z, Nq, d, seed):
+    """Q [1, 1, Nq, d], K [1, 1, Nk, d], V, dO whose scaled scores are z[j] (z: [Nk]) plus
+    products of deviation about 0.3: the first column holds z, the others noise."""
+    g = torch.Generator().manual_seed(seed)
+    Nk = len(z)
+    q, do = (torch.randn(1, 1, Nq, d, generator=g) for _ in "qg")
+    k, v = (torch.randn(1, 1, Nk, d, generator=g) for _ in "kv")
+    q, k = q * 0.5, k * 0.5
+    q[..., 0] = 8.0
+    k[0, 0, :, 0] = torch.tensor(z) * d ** 0.5 / 8.0
+    return [t.bfloat16() for t in (q, k, v, do)]
+
+
+# (cap, visible scores, hidden ones beside them): visible scores down towards the cap, hidden
+# ones on both sides of what a tile takes the polynomial for
+FAR = [(cap, low, hid) for cap, low in ((50.0, -90.0), (60.0, -120.0), (100.0, -95.0), (200.0, -120.0),
+                                        (1000.0, -300.0), (1e4, -300.0))
+       for hid in (0.0, 33.0, -33.0)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("softcap,low,hidden", FAR)
+def test_hidden_document_before_low_scores(softcap, low, hidden, d):
+    """Rows walk a key tile of another document, whose scores would be the larger ones by
+    far, before the tile of their own."""
+    ids = torch.tensor([[0] * 128 + [1] * 128 + [2] * 60 + [3] * 84], dtype=torch.int32)
+    z = [hidden] * 128 + [low] * 128 + [hidden] * 60 + [low] * 84
+    for causal in (False, True):
+        check(*placed(z, 400, d, 1), softcap=softcap, ids=ids, causal=causal)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("softcap,low,hidden", FAR)
+def test_hidden_keys_behind_low_scores(softcap, low, hidden, d):
+    """The first rows of a row tile do not see its last key tile, whose scores would be the
+    larger ones: causal with a position in mid-tile, and keys behind a prefix."""
+    z = [low] * 128 + [hidden] * 64
+    check(*placed(z, 128, d, 2), softcap=softcap, causal=True)
+    z = [low] * 256 + [hidden] * 72
+    check(*placed(z, 328, d, 3), softcap=softcap, causal=True, prefix=[130])
+
+
+@pytest.mark.parametrize("softcap", [60.0, 100.0, 1000.0])
+def test_low_and_hidden_scores_in_one_tile(softcap):
+    """Visible keys of both sizes among hidden ones, document by document."""
+    rng = np.random.default_rng(4)
+    N = 700
+    ids = np.cumsum(rng.random(N) < 0.03).astype(np.int32)
+    z = rng.choice([-1.4 * softcap, -33.0, 0.0, 33.0], size=ids.max() + 1)[ids]
+    check(*placed(z.tolist(), N, 64, 5), softcap=softcap, causal=True,
+          ids=torch.from_numpy(ids)[None])
