@@ -99,12 +99,19 @@ inline CapArgs cap_args(float scale, float softcap) {
   const double* q = taylor ? taylor_q : fit_q;
   const double* qb = taylor ? taylor_q : fit_qb;
   const double* g = taylor ? taylor_g : fit_g;
+  // (Caps far below the scale, in above 1e5, take the last coefficients past float32, and zero
+  // times infinity is a NaN: no product is in such a polynomial's range, zero ones included.)
   double f = 1.0;
+  bool holds = true, holds_b = true;
   for (int i = 0; i < 5; ++i, f *= in * in) {
     c.q[i] = static_cast<float>(q[i] * f * out * in);
+    holds = holds && std::isfinite(c.q[i]);
     if (i < 4) c.qb[i] = static_cast<float>(qb[i] * f * out * in);
     if (i < 3) c.g[i] = static_cast<float>(g[i] * f);
+    holds_b = holds_b && std::isfinite(c.qb[i < 4 ? i : 3]) && std::isfinite(c.g[i < 3 ? i : 2]);
   }
+  if (!holds) c.top = c.poly = -1.f;
+  if (!holds_b) c.top_b = -1.f;
   return c;
 }
 

@@ -11,7 +11,8 @@ subtraction of the maximum and the logarithm: by 2^-19 |x| + 4.3e-5.  LSE may be
 (its rounding, its score and LSE or sum, the exponential), dP - D by 2^-20 of the products that
 make it (d and Nk of them in float32, whose roundings add up like their root), and
   eS = |dS| (2^-8 + 2^-18 |x| + 3e-4) + P dz 2^-20 (|dO| |V|^T + |dO| . |O|)
-(3e-4: the cap's derivative, 1.6e-4, beside eP's).  Then O, dV, dQ and dK are off by
+(3e-4: the cap's derivative, 1.6e-4, beside eP's; and P |dP - D| 2^-21 where that is 1 - tanh^2
+of a float32 tanh, off by 2^-23 at 1, squared, subtracted).  Then O, dV, dQ and dK are off by
 eP |V|, eP^T |dO|, scale eS |K| and scale eS^T |Q| and by their own rounding.  These bounds do
 not presume scores of any size: where all of a row's keys share a large column, its dQ there
 is a difference of large products, each rounded.  The gradients are compared with the
@@ -76,7 +77,8 @@ def check(q, k, v, do, *, causal=False, softcap=0.0, slopes=None, prefix=None, i
             assert_within(gO, rO, eP @ np.abs(Vh), f"O b={b} h={h}")
             dQ, dK, dV = ref.backward(Qh, Kh, Vh, Gh, scale, seen, softcap, sl, O=gO)
             D = (Gh * gO).sum(axis=1, keepdims=True)
-            eS = (np.abs(P * (Gh @ Vh.T - D) * dz) * (HALF + 2.0 ** -18 * ax + 3e-4) +
+            dP = np.abs(P * (Gh @ Vh.T - D))
+            eS = (dP * dz * (HALF + 2.0 ** -18 * ax + 3e-4) + dP * 2.0 ** -21 +
                   P * dz * 2.0 ** -20 * (np.abs(Gh) @ np.abs(Vh).T +
                                          (np.abs(Gh) * np.abs(gO)).sum(axis=1, keepdims=True)))
             g = to64(grads[0][b, h])
@@ -145,3 +147,36 @@ def test_low_and_hidden_scores_in_one_tile(softcap):
     z = rng.choice([-1.4 * softcap, -33.0, 0.0, 33.0], size=ids.max() + 1)[ids]
     check(*placed(z.tolist(), N, 64, 5), softcap=softcap, causal=True,
           ids=torch.from_numpy(ids)[None])
+
+
+# ------------------------------------------------------------------ caps near nothing
+@pytest.mark.parametrize("softcap", [1.1e-9, 1e-8, 1e-7, 5e-7, 1e-6, 1e-3])
+@pytest.mark.parametrize("d", [64, 128])
+def test_zero_queries_under_a_small_cap(softcap, d):
+    """Rows whose every product is zero (padding), beside rows that saturate: equal weights."""
+    g = torch.Generator().manual_seed(6)
+    q, do = (torch.randn(1, 4, 300, d, generator=g).bfloat16() for _ in "qg")
+    k, v = (torch.randn(1, 2, 300, d, generator=g).bfloat16() for _ in "kv")
+    q[:, :, :100] = 0
+    q[:, 1] = 0
+    for causal in (False, True):
+        check(q, k, v, do, softcap=softcap, causal=causal)
+    check(q, k, v, do, softcap=softcap, causal=True, slopes=[0.5, 0.1, 0.0, 0.02])
+
+
+@pytest.mark.parametrize("softcap", [1.1e-9, 1e-7, 1e-6])
+def test_zero_query_under_a_small_cap_over_a_paged_cache(softcap):
+    g = torch.Generator().manual_seed(7)
+    k, v = (torch.randn(40, 2, 16, 64, generator=g).bfloat16() for _ in "kv")
+    q = torch.zeros(1, 4, 1, 64, dtype=torch.bfloat16)
+    q[0, 3] = torch.randn(1, 64, generator=g).bfloat16()
+    table = torch.arange(40, dtype=torch.int32)[None].contiguous()
+    lens = torch.tensor([600], dtype=torch.int32)
+    O, LSE = binding.fwd_tree(*(t.cuda() for t in (q, k, v, table, lens)), softcap=softcap)
+    binding.check_device_error()
+    # every weight is 1 / 600, rounded; so is the output
+    flat = to64(v.transpose(0, 1).reshape(2, 640, 64)[:, :600])
+    for h in range(4):
+        bound = HALF * np.abs(flat[h // 2]).mean(axis=0)[None] * 1.01
+        assert_within(to64(O[0, h]), flat[h // 2].mean(axis=0)[None], bound, f"O h={h}")
+    assert np.abs(to64(LSE) - np.log(600.0)).max() <= 1e-4
