@@ -71,7 +71,7 @@ def check(q, k, v, do, *, causal=False, softcap=0.0, slopes=None, prefix=None, i
             gO, gL = to64(O[b, h]), to64(LSE[b, h])
             assert (gO[empty] == 0).all() and np.isneginf(gL[empty]).all()
             ax = np.where(seen, np.abs(x), 0.0).max(axis=1, keepdims=True)
-            off = np.abs(gL - rL)[~empty] - (1e-4 + 2.0 ** -19 * ax[~empty, 0])
+            off = np.abs(gL[~empty] - rL[~empty]) - (1e-4 + 2.0 ** -19 * ax[~empty, 0])
             assert off.max(initial=0.0) <= 0, f"LSE b={b} h={h}: {off.max():.3e} over its bound"
             eP = P * (HALF + 2.0 ** -18 * ax + 1e-4)
             assert_within(gO, rO, eP @ np.abs(Vh), f"O b={b} h={h}")
@@ -180,3 +180,65 @@ def test_zero_query_under_a_small_cap_over_a_paged_cache(softcap):
         bound = HALF * np.abs(flat[h // 2]).mean(axis=0)[None] * 1.01
         assert_within(to64(O[0, h]), flat[h // 2].mean(axis=0)[None], bound, f"O h={h}")
     assert np.abs(to64(LSE) - np.log(600.0)).max() <= 1e-4
+
+
+# ------------------------------------------------------------------ many units a CTA
+def rows_of_documents(B, N, seed, gaps):
+    """Documents of 1 to 500 tokens with runs of padding (first, last) between them."""
+    rng = np.random.default_rng(seed)
+    ids = np.stack([np.cumsum(rng.random(N) < 0.01) for _ in range(B)]).astype(np.int32)
+    for b in range(B):
+        for first, last in gaps:
+            ids[b, min(N, first + 40 * b):min(N, last + 40 * b)] = -1
+    return torch.from_numpy(ids)
+
+
+def tensors(B, H, Hkv, Nq, Nk, d, seed):
+    g = torch.Generator().manual_seed(seed)
+    q, do = (torch.randn(B, H, Nq, d, generator=g) for _ in "qg")
+    k, v = (torch.randn(B, Hkv, Nk, d, generator=g) for _ in "kv")
+    return [t.bfloat16() for t in (q * 1.5, k * 1.5, v, do)]
+
+
+MODS = [{}, {"softcap": 20.0}, {"slopes": True}, {"softcap": 20.0, "slopes": True}]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("mods", MODS, ids=["mask", "cap", "bias", "both"])
+def test_several_units_a_block(mods, d):
+    """384 forward, 192 dK/dV and 768 dQ units for 148 SMs, ranked by cost; dead units, and
+    units with one live row tile, among them."""
+    B, H, Hkv, N = 4, 16, 4, 1500
+    kw = dict(mods)
+    if "slopes" in kw:
+        kw["slopes"] = [2.0 ** (-h / 2) for h in range(1, H + 1)]
+    ids = rows_of_documents(B, N, 8, [(250, 640), (900, 1300)])
+    check(*tensors(B, H, Hkv, N, N, d, 9), ids=ids, causal=True, heads=(4, 5, 6, 7),
+          sequences=(0, 3), **kw)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("mods", MODS[:2], ids=["mask", "cap"])
+def test_queries_in_front_of_the_first_key(mods, d):
+    """Nq > Nk with documents: whole units, and the first row tile of one (rows 256 to 383 see
+    nothing, those behind them do), lie in front of the first key."""
+    B, H, Hkv, Nk = 3, 16, 8, 1100
+    check(*tensors(B, H, Hkv, Nk + 384, Nk, d, 10), heads=(2, 3), sequences=(0, 2),
+          ids=rows_of_documents(B, Nk, 11, [(300, 700)]), **mods)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_units_too_many_to_be_ranked(d):
+    """More than 256 row tile pairs over the batch: dealt in index order."""
+    B, N = 70, 1000
+    ids = rows_of_documents(B, N, 12, [(100, 500)])
+    for causal in (False, True):
+        check(*tensors(B, 2, 1, N, N, d, 13), ids=ids, causal=causal, softcap=20.0,
+              sequences=(0, 9, 69))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_several_units_without_documents(d):
+    check(*tensors(2, 32, 16, 2000, 2000, d, 14), causal=True, softcap=20.0, prefix=[900, 0],
+          heads=(0, 1), sequences=(0, 1))
+    check(*tensors(3, 16, 4, 900, 1900, d, 15), heads=(12, 13, 14, 15), sequences=(2,))
