@@ -556,14 +556,69 @@ fa_status bwd_mod_impl(const void* Q, const void* K, const void* V, const void* 
 }
 
 // ------------------------------------------------------------------ rotary positions
+// A strided view of rows, in bytes: rows of `row` bytes at p + sum of i_k st[k], i_k < n[k].
+struct View {
+  const void* p;
+  long long row, n[3], st[3];
+  long long span() const {
+    long long last = row;
+    for (int k = 0; k < 3; ++k) last += (n[k] - 1) * st[k];
+    return last;
+  }
+  // the same without the dimensions that step by multiples of `period`
+  long long span_within(long long period) const {
+    long long last = row;
+    for (int k = 0; k < 3; ++k)
+      if (n[k] > 1 && st[k] % period != 0) last += (n[k] - 1) * st[k];
+    return last;
+  }
+};
+
+View flat_view(const void* p, size_t bytes) {
+  return View{p, static_cast<long long>(bytes), {1, 1, 1}, {0, 0, 0}};
+}
+
+// Whether two views may share a byte.  They do not if they lie apart, or if their rows,
+// taken modulo a stride, do: heads of one fused buffer lie apart modulo its token stride,
+// slices of a head-major one modulo its batch stride.
+bool may_share(const View& x, const View& y) {
+  if (!overlaps(x.p, x.span(), y.p, y.span())) return false;
+  for (const View* v : {&x, &y}) {
+    for (int k = 0; k < 3; ++k) {
+      const long long period = v->st[k];
+      if (v->n[k] <= 1 || period <= 0) continue;
+      const long long nx = x.span_within(period), ny = y.span_within(period);
+      long long at = (static_cast<const char*>(y.p) - static_cast<const char*>(x.p)) % period;
+      if (at < 0) at += period;
+      if (at >= nx && at + ny <= period) return false;
+    }
+  }
+  return true;
+}
+
+// Whether rows of a view may share a byte with one another: each stride has to step past
+// all that the smaller ones cover.
+bool rows_may_share(const View& x) {
+  long long cover = x.row;
+  bool done[3] = {x.n[0] <= 1, x.n[1] <= 1, x.n[2] <= 1};
+  for (int step = 0; step < 3; ++step) {
+    int k = -1;
+    for (int i = 0; i < 3; ++i)
+      if (!done[i] && (k < 0 || x.st[i] < x.st[k])) k = i;
+    if (k < 0) break;
+    if (x.st[k] < cover) return true;
+    cover += (x.n[k] - 1) * x.st[k];
+    done[k] = true;
+  }
+  return false;
+}
+
 // One tensor of heads of a rotary call.  strides: {in b, h, n, out b, h, n} in elements, or
-// null for contiguous [B,heads,N,d] on both sides.
+// null for contiguous [B,heads,N,d] on both sides.  view: the input's and the output's.
 fa_status rotary_tensor(const char* name, const void* in, void* out, int heads, int B, int N,
                         int d, const long long* strides, int elem, fa::RotaryTensor* x,
-                        size_t extent[2], bool* in_place) {
+                        View view[2]) {
   *x = fa::RotaryTensor{};
-  extent[0] = extent[1] = 0;
-  *in_place = true;
   if (heads < 0) return fail(FA_ERR_INVALID_ARG, "%s has %d heads", name, heads);
   if (heads == 0) return FA_OK;
   if (static_cast<long long>(heads) * N > 0x7fffffffll / B)
@@ -576,23 +631,24 @@ fa_status rotary_tensor(const char* name, const void* in, void* out, int heads, 
   const long long dense[6] = {dense_b, dense_h, dense_n, dense_b, dense_h, dense_n};
   const long long* s = strides != nullptr ? strides : dense;
   for (int o = 0; o < 2; ++o) {
-    const long long n[3] = {B, heads, N};
+    View& v = view[o];
+    v = View{o == 0 ? in : out, static_cast<long long>(d) * elem, {B, heads, N}, {}};
     long long last = d;
     for (int k = 0; k < 3; ++k) {
       const long long st = s[3 * o + k];
       if (st < 0 || st > (1ll << 40))
         return fail(FA_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40]", name);
-      if (n[k] > 1 && st > ((1ll << 46) - last) / (n[k] - 1))
+      if (v.n[k] > 1 && st > ((1ll << 46) - last) / (v.n[k] - 1))
         return fail(FA_ERR_INVALID_ARG, "%s spans too many elements", name);
-      // rows of the output must not share elements
-      if (o == 1 && n[k] > 1 && st < d)
-        return fail(FA_ERR_INVALID_ARG, "%s: an output stride is below d", name);
-      last += (n[k] - 1) * st;
+      last += (v.n[k] - 1) * st;
+      v.st[k] = st * elem;
     }
-    extent[o] = static_cast<size_t>(last) * elem;
   }
-  *in_place = in == out && s[0] == s[3] && s[1] == s[4] && s[2] == s[5];
-  if (!*in_place && overlaps(in, extent[0], out, extent[1]))
+  if (rows_may_share(view[1]))
+    return fail(FA_ERR_INVALID_ARG, "%s: rows of the output overlap one another", name);
+  bool in_place = in == out;
+  for (int k = 0; k < 3; ++k) in_place = in_place && (view[0].n[k] <= 1 || s[k] == s[3 + k]);
+  if (!in_place && may_share(view[0], view[1]))
     return fail(FA_ERR_INVALID_ARG, "%s overlaps its output and is not the same tensor", name);
   *x = fa::RotaryTensor{in, out, heads, s[0], s[1], s[2], s[3], s[4], s[5]};
   return FA_OK;
@@ -619,21 +675,25 @@ fa_status rotary_impl(const void* Q, void* Q_out, const void* K, void* K_out,
                 static_cast<long long>(B) * N);
   if (B == 0 || N == 0) return FA_OK;
   fa::RotaryArgs a{};
-  size_t qx[2], kx[2];
-  bool q_in_place, k_in_place;
-  FA_TRY(rotary_tensor("Q", Q, Q_out, H, B, N, d, q_strides, elem, &a.x[0], qx, &q_in_place));
-  FA_TRY(rotary_tensor("K", K, K_out, Hkv, B, N, d, k_strides, elem, &a.x[1], kx, &k_in_place));
+  View q[2], k[2];
+  FA_TRY(rotary_tensor("Q", Q, Q_out, H, B, N, d, q_strides, elem, &a.x[0], q));
+  FA_TRY(rotary_tensor("K", K, K_out, Hkv, B, N, d, k_strides, elem, &a.x[1], k));
   if (H == 0 && Hkv == 0) return FA_OK;
   if (H > 0 && Hkv > 0) {
-    if (Q_out == K_out) return fail(FA_ERR_INVALID_ARG, "Q and K have the same output");
-    // (heads of one fused buffer turned in place interleave, and so may two outputs)
-    if ((!q_in_place && overlaps(Q_out, qx[1], K, kx[0])) ||
-        (!k_in_place && overlaps(K_out, kx[1], Q, qx[0])))
+    if (may_share(q[1], k[1])) return fail(FA_ERR_INVALID_ARG, "the outputs overlap");
+    if (may_share(q[1], k[0]) || may_share(k[1], q[0]))
       return fail(FA_ERR_INVALID_ARG, "an output overlaps the other input");
   }
   if (R > 0 && inv_freq == nullptr) return fail(FA_ERR_INVALID_ARG, "inv_freq is NULL");
   if (!aligned4(inv_freq) || !aligned4(positions))
     return fail(FA_ERR_INVALID_ARG, "inv_freq and positions must be 4-byte aligned");
+  const View freq = flat_view(inv_freq, static_cast<size_t>(R / 2) * 4);
+  const View pos = flat_view(positions, static_cast<size_t>(B) * N * 4);
+  for (const View* out : {H > 0 ? &q[1] : nullptr, Hkv > 0 ? &k[1] : nullptr}) {
+    if (out == nullptr) continue;
+    if ((R > 0 && may_share(*out, freq)) || (positions != nullptr && may_share(*out, pos)))
+      return fail(FA_ERR_INVALID_ARG, "an output overlaps inv_freq or positions");
+  }
   a.inv_freq = inv_freq;
   a.positions = positions;
   a.first = first;

@@ -365,7 +365,10 @@ FA_API fa_status fa_bwd_mod(const void* Q, const void* K, const void* V, const v
  * gradient of the inputs is the same call on the gradient of the outputs.
  *   Q, K       in : [B,H,N,d] and [B,Hkv,N,d]; H or Hkv = 0 leaves that tensor out
  *   Q_out, K_out out: the same shapes; may be the input itself (same pointer and strides),
- *                and must not overlap it otherwise, nor the other input
+ *                and must share no element with it otherwise, nor with the other tensor's
+ *                input or output, inv_freq or positions; rows of an output must not share
+ *                elements.  Views are taken to share some unless they lie apart in memory, or
+ *                modulo one of their strides (heads of one fused buffer do)
  *   inv_freq   in : [R/2] float32 on the device (frequency scaling for long contexts is a
  *                matter of its values and of mscale)
  *   positions  in : [B,N] int32 on the device, any values; or NULL: token n of every

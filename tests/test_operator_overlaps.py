@@ -1,0 +1,108 @@
+"""Buffers that a call writes and another argument shares: refused on the host (no GPU; an
+accepted call gets as far as asking for a device)."""
+import ctypes
+
+import pytest
+import torch
+
+from exact_io_aware_64_b200 import binding
+
+BAD = binding.FA_ERR_INVALID_ARG
+BASE = 1 << 40
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="its addresses are made up")
+
+
+def refused(fn, args):
+    lib = binding.lib()
+    status = getattr(lib, fn)(*args)
+    msg = lib.fa_last_error_message().decode()
+    assert (status == BAD) == bool("overlap" in msg or "share" in msg or "same output" in msg), msg
+    return status == BAD
+
+
+# ------------------------------------------------------------------ rotary
+class View:
+    """A strided view of elements of a buffer: offset and strides in elements."""
+
+    def __init__(self, buf, at, b, h, n):
+        self.buf, self.at, self.st = buf, at, (b, h, n)
+
+
+def rotary(q, qo, k, ko, *, B=2, H=4, Hkv=2, N=10, d=64, elem=2, pos=None, freq=BASE + (9 << 32)):
+    def ptr(v):
+        return BASE + (v.buf << 32) + v.at * elem
+
+    qs, ks = ((ctypes.c_longlong * 6)(*x.st, *y.st) for x, y in ((q, qo), (k, ko)))
+    return refused("fa_rotary" if elem == 2 else "fa_rotary_f32",
+                   [ptr(q), ptr(qo), ptr(k), ptr(ko), freq, pos, 0, B, H, Hkv, N, d, d, 0, 0, 1.0,
+                    qs, ks, None])
+
+
+def dense(buf, heads, N=10, d=64, at=0):
+    return View(buf, at, heads * N * d, N * d, d)
+
+
+def fused(buf, first, heads, N=10, d=64):
+    """Heads from ``first`` on of a [B, N, heads, d] buffer."""
+    return View(buf, first * d, N * heads * d, d, heads * d)
+
+
+@no_gpu
+@pytest.mark.parametrize("elem", [2, 4])
+def test_rotary_layouts_that_share_nothing(elem):
+    q, k = fused(0, 0, 8), fused(0, 4, 8)
+    kw = {"elem": elem}
+    assert not rotary(dense(0, 4), dense(1, 4), dense(2, 2), dense(3, 2), **kw)
+    # heads of one fused buffer, both in place, one of them, or neither
+    assert not rotary(q, q, k, k, **kw)
+    assert not rotary(q, q, k, dense(1, 2), **kw)
+    assert not rotary(q, dense(1, 4), k, k, **kw)
+    assert not rotary(q, fused(1, 0, 8), k, fused(1, 4, 8), **kw)
+    # queries turned into heads of the buffer that nothing else uses
+    assert not rotary(fused(0, 0, 16), fused(0, 8, 16), fused(0, 4, 16), fused(0, 4, 16), **kw)
+    # head-major: [B, heads, N, d] of both, one after the other in every sequence
+    q, k = View(0, 0, 6 * 640, 640, 64), View(0, 4 * 640, 6 * 640, 640, 64)
+    assert not rotary(q, q, k, k, **kw)
+    # one token in place: the token's own stride says nothing
+    assert not rotary(dense(0, 4, N=1), View(0, 0, 256, 64, 9999), dense(1, 2, N=1), dense(2, 2, N=1),
+                      N=1, **kw)
+    # query and key of a head side by side: [B, N, heads, 2, d]
+    q, k = View(0, 0, 10 * 512, 128, 512), View(0, 64, 10 * 512, 128, 512)
+    assert not rotary(q, q, k, k, H=4, Hkv=4, **kw)
+
+
+@no_gpu
+@pytest.mark.parametrize("elem", [2, 4])
+def test_rotary_outputs_over_other_arguments(elem):
+    x, f = dense(0, 4), fused(0, 0, 8)
+    kw = {"elem": elem}
+    # the same tensor as query, in place, and as key, elsewhere: read while it is written
+    assert rotary(x, x, x, dense(1, 4), H=4, Hkv=4, **kw)
+    assert rotary(x, dense(1, 4), x, x, H=4, Hkv=4, **kw)
+    assert rotary(f, f, f, dense(1, 4), H=4, Hkv=4, **kw)
+    # heads that both tensors have, in place: turned twice
+    assert rotary(f, f, fused(0, 3, 8), fused(0, 3, 8), **kw)
+    assert rotary(x, x, View(0, 640, *x.st), View(0, 640, *x.st), **kw)
+    # outputs with heads in common
+    assert rotary(dense(0, 4), fused(2, 0, 8), dense(1, 2), fused(2, 3, 8), **kw)
+    assert rotary(dense(0, 4), dense(2, 4), dense(1, 2), dense(2, 2, at=100), **kw)
+    # one element in common
+    assert rotary(dense(0, 4), dense(2, 4), dense(1, 2), dense(2, 2, at=2 * 4 * 640 - 1), **kw)
+
+
+@no_gpu
+def test_rotary_output_rows_that_share_elements():
+    q, k = dense(0, 4), dense(2, 2)
+    for st in ((2560, 64, 64), (2560, 640, 32), (64, 640, 64), (640, 640, 64), (0, 640, 64),
+               (2559, 640, 64)):
+        assert rotary(q, View(1, 0, *st), k, dense(3, 2))
+    for st in ((2560, 640, 64), (64, 640, 2560 * 8), (64, 128, 512), (1 << 30, 640, 64)):
+        assert not rotary(q, View(1, 0, *st), k, dense(3, 2))
+
+
+@no_gpu
+def test_rotary_output_over_positions_and_frequencies():
+    args = dense(0, 4), dense(1, 4), dense(2, 2), dense(3, 2)
+    end = BASE + (1 << 32) + 2 * 4 * 640 * 2
+    assert not rotary(*args, pos=end) and rotary(*args, pos=end - 4)
+    assert not rotary(*args, freq=end) and rotary(*args, freq=end - 4)
