@@ -12,6 +12,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "fa.h"
@@ -177,6 +178,28 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool overlaps(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + b_bytes && y < x + a_bytes;
+}
+
+// A named argument's bytes (null or empty: absent).
+struct Buf {
+  const char* name;
+  const void* p;
+  size_t n;
+};
+
+// No output (or workspace) shares a byte with an input or another output.
+fa_status check_apart(std::initializer_list<Buf> outs, std::initializer_list<Buf> ins) {
+  for (const Buf* o = outs.begin(); o != outs.end(); ++o) {
+    if (o->p == nullptr || o->n == 0) continue;
+    auto meets = [&](const Buf& x) {
+      return x.p != nullptr && x.n > 0 && overlaps(o->p, o->n, x.p, x.n);
+    };
+    for (const Buf& in : ins)
+      if (meets(in)) return fail(FA_ERR_INVALID_ARG, "%s overlaps %s", o->name, in.name);
+    for (const Buf* x = outs.begin(); x != o; ++x)
+      if (meets(*x)) return fail(FA_ERR_INVALID_ARG, "%s overlaps %s", o->name, x->name);
+  }
+  return FA_OK;
 }
 
 // Longest sequence any call accepts: every length rounded up to whole 256-row units
@@ -791,11 +814,15 @@ fa_status tree_impl(const void* Q, const void* K_cache, const void* V_cache, voi
                 need);
   const size_t qb = static_cast<size_t>(B) * H * T * d * 2;
   const size_t cb = static_cast<size_t>(num_pages) * Hkv * page * d * 2;
-  if (overlaps(O, qb, Q, qb) || overlaps(O, qb, K_cache, cb) || overlaps(O, qb, V_cache, cb))
-    return fail(FA_ERR_INVALID_ARG, "O overlaps an input");
-  if (overlaps(workspace, need, Q, qb) || overlaps(workspace, need, K_cache, cb) ||
-      overlaps(workspace, need, V_cache, cb) || overlaps(workspace, need, O, qb))
-    return fail(FA_ERR_INVALID_ARG, "the workspace overlaps a tensor");
+  const size_t rows = static_cast<size_t>(B) * T, i32 = sizeof(int);
+  FA_TRY(check_apart({{"O", O, qb}, {"LSE", LSE, rows * H * 4}, {"the workspace", workspace, need}},
+                     {{"Q", Q, qb},
+                      {"K_cache", K_cache, cb},
+                      {"V_cache", V_cache, cb},
+                      {"block_table", block_table, static_cast<size_t>(B) * max_pages * i32},
+                      {"cache_lens", cache_lens, B * i32},
+                      {"seqlens_q", seqlens_q, B * i32},
+                      {"tree_mask", tree_mask, rows * 8}}));
   DeviceInfo dev;
   FA_TRY(device_info(&dev));
   FA_TRY(require_sm100(dev));

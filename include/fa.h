@@ -412,8 +412,9 @@ FA_API size_t fa_fwd_tree_workspace_bytes(int B, int H, int Hkv, int T, int d);
  *        token u (its ancestors and itself; bits from n_b on are ignored).  NULL is a
  *        chain: token t sees drafted tokens 0 .. t.  Every row sees all tokens before
  *        the drafted ones.
- *   O    out: [B,H,T,d] bf16, must not overlap an input;  LSE out: [B,H,T] float32 or NULL
+ *   O    out: [B,H,T,d] bf16;  LSE out: [B,H,T] float32 or NULL
  *   softcap as in fa_fwd_mod;  workspace: fa_fwd_tree_workspace_bytes bytes, 16-byte aligned
+ *        (O, LSE and workspace must not overlap one another or any input)
  *   T <= 64; B <= 4096; page 8, 16, 32, 64 or a multiple of 128; d 64 or 128
  * A row that sees no key gets O = 0 and LSE = -inf.  Slots of a page behind its sequence's
  * end may hold anything.  A sequence whose lengths are out of range (cache_lens[b] outside

@@ -106,3 +106,39 @@ def test_rotary_output_over_positions_and_frequencies():
     end = BASE + (1 << 32) + 2 * 4 * 640 * 2
     assert not rotary(*args, pos=end) and rotary(*args, pos=end - 4)
     assert not rotary(*args, freq=end) and rotary(*args, freq=end - 4)
+
+
+# ------------------------------------------------------------------ paged cache
+TREE = {"Q": 1, "K": 2, "V": 3, "O": 4, "LSE": 5, "table": 6, "lens": 7, "sq": 8, "mask": 9,
+        "ws": 10}
+# B=3 H=4 Hkv=2 T=5 pages=50 page=16 max_pages=20 d=64
+TREE_BYTES = {"Q": 3 * 4 * 5 * 128, "K": 50 * 2 * 16 * 128, "V": 50 * 2 * 16 * 128,
+              "O": 3 * 4 * 5 * 128, "LSE": 3 * 4 * 5 * 4, "table": 3 * 20 * 4, "lens": 12,
+              "sq": 12, "mask": 3 * 5 * 8}
+
+
+def tree(**at):
+    ptr = {n: at.get(n, BASE + (i << 32)) for n, i in TREE.items()}
+    need = binding.tree_workspace_bytes(3, 4, 2, 5, 64)
+    return refused("fa_fwd_tree", [*list(ptr.values())[:9], 3, 4, 2, 5, 50, 16, 20, 64, 0.1, 0.0,
+                                   ptr["ws"], need, None])
+
+
+@no_gpu
+@pytest.mark.parametrize("out", ["O", "LSE", "ws"])
+def test_tree_outputs_over_other_arguments(out):
+    assert not tree() and not tree(sq=None, mask=None, LSE=None)
+    size = dict(TREE_BYTES, ws=binding.tree_workspace_bytes(3, 4, 2, 5, 64))
+    for name, i in TREE.items():
+        if name == out:
+            continue
+        at = BASE + (i << 32)
+        last = at + (size[name] - 1) // 16 * 16  # (aligned as every output has to be)
+        behind = at + (size[name] + 15) // 16 * 16
+        assert tree(**{out: at}), name
+        assert tree(**{out: last}), name
+        assert not tree(**{out: behind}), name
+        # and from in front
+        mine = (size[out] + 15) // 16 * 16
+        assert tree(**{out: at - mine + 16}) == (size[out] > mine - 16), name
+        assert not tree(**{out: at - mine}), name
