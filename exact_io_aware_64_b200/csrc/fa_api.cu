@@ -493,8 +493,15 @@ fa_status fwd_mod_impl(const void* Q, const void* K, const void* V, void* O, flo
   if (!aligned4(LSE)) return fail(FA_ERR_INVALID_ARG, "LSE is not 4-byte aligned");
   const size_t qb = static_cast<size_t>(B) * H * Nq * d * 2;
   const size_t kb = static_cast<size_t>(B) * m.Hkv * Nk * d * 2;
-  if (overlaps(O, qb, Q, qb) || overlaps(O, qb, K, kb) || overlaps(O, qb, V, kb))
-    return fail(FA_ERR_INVALID_ARG, "O overlaps an input");
+  const size_t i32 = sizeof(int), keys = static_cast<size_t>(B) * Nk * i32;
+  FA_TRY(check_apart({{"O", O, qb}, {"LSE", LSE, static_cast<size_t>(B) * H * Nq * 4}},
+                     {{"Q", Q, qb},
+                      {"K", K, kb},
+                      {"V", V, kb},
+                      {"slopes", m.slopes, H * i32},
+                      {"prefix", m.prefix, B * i32},
+                      {"doc_start", m.doc_start, keys},
+                      {"doc_end", m.doc_end, keys}}));
   DeviceInfo dev;
   FA_TRY(device_info(&dev));
   FA_TRY(require_sm100(dev));
@@ -541,21 +548,19 @@ fa_status bwd_mod_impl(const void* Q, const void* K, const void* V, const void* 
   if (workspace_bytes < need)
     return fail(FA_ERR_INVALID_ARG, "workspace has %zu bytes, %zu needed", workspace_bytes,
                 need);
-  struct Buf {
-    const void* p;
-    size_t n;
-  };
-  const size_t lb = static_cast<size_t>(B) * H * Nq * 4;
-  const Buf ins[6] = {{Q, qb}, {K, kb}, {V, kb}, {O, qb}, {dO, qb}, {LSE, lb}};
-  const Buf outs[4] = {{dQ, qb}, {dK, kb}, {dV, kb}, {workspace, need}};
-  for (int i = 0; i < 4; ++i) {
-    for (const Buf& in : ins)
-      if (overlaps(outs[i].p, outs[i].n, in.p, in.n))
-        return fail(FA_ERR_INVALID_ARG, "a gradient or the workspace overlaps an input");
-    for (int k = 0; k < i; ++k)
-      if (overlaps(outs[i].p, outs[i].n, outs[k].p, outs[k].n))
-        return fail(FA_ERR_INVALID_ARG, "gradients and workspace overlap each other");
-  }
+  const size_t i32 = sizeof(int), keys = static_cast<size_t>(B) * Nk * i32;
+  FA_TRY(check_apart(
+      {{"dQ", dQ, qb}, {"dK", dK, kb}, {"dV", dV, kb}, {"the workspace", workspace, need}},
+      {{"Q", Q, qb},
+       {"K", K, kb},
+       {"V", V, kb},
+       {"O", O, qb},
+       {"dO", dO, qb},
+       {"LSE", LSE, static_cast<size_t>(B) * H * Nq * 4},
+       {"slopes", m.slopes, H * i32},
+       {"prefix", m.prefix, B * i32},
+       {"doc_start", m.doc_start, keys},
+       {"doc_end", m.doc_end, keys}}));
   DeviceInfo dev;
   FA_TRY(device_info(&dev));
   FA_TRY(require_sm100(dev));

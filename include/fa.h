@@ -319,7 +319,8 @@ FA_API fa_status fa_doc_ranges(const int* doc_ids, int* doc_start, int* doc_end,
  *   ranges are given, p_i and j lie in the same document (a row with p_i < 0 in none);
  *   O = softmax over the visible keys of x times V, LSE = log sum exp x.
  *   Q   in : [B,H,Nq,d] bf16;  K, V in : [B,Hkv,Nk,d] bf16, H a multiple of Hkv
- *   O   out: [B,H,Nq,d] bf16, must not overlap Q, K or V;  LSE out: [B,H,Nq] float32 or NULL
+ *   O   out: [B,H,Nq,d] bf16;  LSE out: [B,H,Nq] float32 or NULL (neither over the other or
+ *                over any input)
  *   slopes  in : [H] float32 or NULL (finite; they are constants, no gradient is formed)
  *   prefix  in : [B] int32 or NULL: keys below it are visible to every row of sequence b
  *                (of the same document); needs causal = 1; taken as min(prefix, Nk), and

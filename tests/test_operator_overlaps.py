@@ -142,3 +142,41 @@ def test_tree_outputs_over_other_arguments(out):
         mine = (size[out] + 15) // 16 * 16
         assert tree(**{out: at - mine + 16}) == (size[out] > mine - 16), name
         assert not tree(**{out: at - mine}), name
+
+
+# ------------------------------------------------------------------ modified scores
+MOD = {"Q": 1, "K": 2, "V": 3, "O": 4, "LSE": 5, "slopes": 6, "prefix": 7, "start": 8, "end": 9,
+       "dO": 10, "dQ": 11, "dK": 12, "dV": 13, "ws": 14}
+# B=3 H=4 Hkv=2 Nq=20 Nk=50 d=64
+MOD_BYTES = {**dict.fromkeys(("Q", "O", "dO", "dQ"), 3 * 4 * 20 * 128),
+             **dict.fromkeys(("K", "V", "dK", "dV"), 3 * 2 * 50 * 128), "LSE": 3 * 4 * 20 * 4,
+             "slopes": 16, "prefix": 12, "start": 3 * 50 * 4, "end": 3 * 50 * 4}
+SIZES = [3, 4, 2, 20, 50, 64, 0.1, 1, 0.0]
+
+
+def mod(backward, **at):
+    p = {n: at.get(n, BASE + (i << 32)) for n, i in MOD.items()}
+    mods = [p[n] for n in ("slopes", "prefix", "start", "end")]
+    if not backward:
+        return refused("fa_fwd_mod", [*(p[n] for n in ("Q", "K", "V", "O", "LSE")), *mods, *SIZES,
+                                      None])
+    return refused("fa_bwd_mod", [*(p[n] for n in ("Q", "K", "V", "O", "dO", "LSE", "dQ", "dK", "dV")),
+                                  *mods, *SIZES, p["ws"], binding.workspace_bytes(3, 4, 20, 64),
+                                  None])
+
+
+@no_gpu
+@pytest.mark.parametrize("backward,out", [(False, "O"), (False, "LSE"), (True, "dQ"), (True, "dK"),
+                                          (True, "dV"), (True, "ws")])
+def test_mod_outputs_over_other_arguments(backward, out):
+    assert not mod(backward)
+    assert not mod(backward, slopes=None, prefix=None, start=None, end=None)
+    size = dict(MOD_BYTES, ws=binding.workspace_bytes(3, 4, 20, 64))
+    for name, i in MOD.items():
+        if name == out or (not backward and name in ("dO", "dQ", "dK", "dV", "ws")):
+            continue
+        at = BASE + (i << 32)
+        assert mod(backward, **{out: at}), name
+        assert mod(backward, **{out: at + (size[name] - 1) // 16 * 16}), name
+        assert not mod(backward, **{out: at + (size[name] + 15) // 16 * 16}), name
+        assert not mod(backward, **{out: at - (size[out] + 15) // 16 * 16}), name
