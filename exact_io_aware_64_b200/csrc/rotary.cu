@@ -8,8 +8,8 @@
 // Bound: HBM, each element read and written once.  A float32 product position * inv_freq
 // is off by 2^-24 of the angle, 0.006 rad at 10^5 rad, so the angle is formed in float64,
 // reduced to a fraction of a turn there, and only the fraction goes to float32 (error of
-// the angle 1e-7 rad).  That costs a few float64 operations and one sincospi per (token,
-// pair), so it must not be repeated for every head.
+// the angle 1e-7 rad at any position).  That costs a few float64 operations and one sincospi
+// per (token, pair), so it must not be repeated for every head.
 //
 // Vector form (R, strides and pointers allow 16-byte pieces): a thread owns one piece of a
 // head row at one token, forms its 2 to 8 angles once, in registers, and turns that piece of
@@ -37,10 +37,16 @@ constexpr int kMaxTokens = 16;  // tokens of one block
 constexpr int kUnroll = 4;      // heads whose loads a thread has in flight
 constexpr long long kStreamBytes = 96ll << 20;  // in and out: about the L2's size
 
-// cos and sin (times m) of pair k at flat token tok.
+// cos and sin (times m) of pair k at position pos.  Both products' roundings are carried along
+// (fma): at 2^40 that of the position's alone is up to 1e-4 rad.
 __device__ __forceinline__ float2 angle(const RotaryArgs& a, double pos, int k) {
-  const double turns = pos * (static_cast<double>(a.inv_freq[k]) * 0.15915494309189533577);
-  const float f = static_cast<float>(2.0 * (turns - rint(turns)));
+  constexpr double kTurn = 0.15915494309189535, kTurnLow = -9.839338337591243e-18;  // 1 / (2 pi)
+  const double inv = static_cast<double>(a.inv_freq[k]);
+  const double per = inv * kTurn;
+  const double per_low = fma(inv, kTurn, -per) + inv * kTurnLow;
+  const double turns = pos * per;
+  const double low = fma(pos, per_low, fma(pos, per, -turns));
+  const float f = static_cast<float>(2.0 * (turns - rint(turns) + low));
   float s, c;
   sincospif(f, &s, &c);
   return make_float2(c * a.mscale, s * a.mscale * a.sign);

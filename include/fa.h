@@ -379,8 +379,9 @@ FA_API fa_status fa_bwd_mod(const void* Q, const void* K, const void* V, const v
  *                out token} of strides in elements, or NULL for contiguous tensors; the
  *                elements of a row are contiguous.  (A packed [tokens,H,d] tensor is B = 1
  *                with strides {0, d, H*d}; a slice of a fused projection works as it is.)
- * Angles are formed in float64 and cos and sin in float32 (fa_rotary_f32: outputs within a
- * few float32 roundings for any position).  One kernel on `stream`; any alignment, 16-byte
+ * Angles are formed in float64 with the roundings of their products carried along, cos and
+ * sin in float32 (fa_rotary_f32: outputs within a few float32 roundings at any position that
+ * the call takes, first from -2^40 to 2^40, while |position * inv_freq| < 2^52).  One kernel on `stream`; any alignment, 16-byte
  * aligned rows run fastest.
  */
 FA_API fa_status fa_rotary(const void* Q, void* Q_out, const void* K, void* K_out,
