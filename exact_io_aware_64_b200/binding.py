@@ -686,7 +686,9 @@ def _rotary(Q, K, inv_freq, positions, first, interleaved, mscale, Q_out, K_out,
     packed = Q.dim() == 3
     if not packed and Q.dim() != 4:
         raise ValueError("Q must be [B, heads, N, d] or packed [tokens, heads, d]")
-    Q_out = torch.empty_like(Q) if Q_out is None else Q_out
+    # (contiguous whatever Q's strides: what the attention calls take)
+    dense = torch.contiguous_format
+    Q_out = torch.empty_like(Q, memory_format=dense) if Q_out is None else Q_out
     q_shape = Q.shape
     qs = ks = None
     if packed or not (Q.is_contiguous() and _like(Q_out, q_shape, dtype, index)):
@@ -701,7 +703,7 @@ def _rotary(Q, K, inv_freq, positions, first, interleaved, mscale, Q_out, K_out,
         Hkv = k_shape[1] if len(k_shape) > 1 else 0
         if k_shape != ((N, Hkv, d) if packed else (B, Hkv, N, d)):
             raise ValueError("Q and K must agree in batch, tokens and head dimension")
-        K_out = torch.empty_like(K) if K_out is None else K_out
+        K_out = torch.empty_like(K, memory_format=dense) if K_out is None else K_out
         if packed or not (_like(K, k_shape, dtype, index) and _like(K_out, k_shape, dtype, index)):
             ks = _rotary_strides("K", K, K_out, dtype, index)
     elif K_out is not None:
@@ -727,8 +729,10 @@ def rotary(Q: torch.Tensor, K: Optional[torch.Tensor], inv_freq: torch.Tensor,
     through ``fa_rotary`` (bf16) or ``fa_rotary_f32``; packed [tokens, heads, d] tensors
     too.  The first 2 * len(inv_freq) elements of each head are turned in pairs (k, k + R/2),
     or (2k, 2k + 1) when ``interleaved``, by position * inv_freq[k]; positions [B, N] (packed:
-    [tokens]) int32, or ``first`` + the token's number.  Any strides with contiguous rows;
-    ``Q_out=Q, K_out=K`` works in place.  Returns (Q_out, K_out)."""
+    [tokens]) int32, or ``first`` + the token's number.  Any strides with contiguous rows
+    (a slice of a fused projection as it is); ``Q_out=Q, K_out=K`` works in place, and outputs
+    that are not given are contiguous, as the attention calls take them.  Returns (Q_out,
+    K_out)."""
     return _rotary(Q, K, inv_freq, positions, first, interleaved, mscale, Q_out, K_out, 0, stream)
 
 
