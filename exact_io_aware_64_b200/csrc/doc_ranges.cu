@@ -77,8 +77,9 @@ __device__ int block_all(int v, int* warp_val) {
 }
 
 __global__ void __launch_bounds__(kThreads)
-    doc_ranges_kernel(const int* __restrict__ ids, int* __restrict__ start,
-                      int* __restrict__ end, int N) {
+    doc_ranges_kernel(const int* ids, int* start, int* end, int N) {
+  // (ids is not __restrict__: loads of what a kernel may never see written could be moved in
+  // front of the wait below, while an earlier kernel still writes the ids)
   __shared__ int warp_val[kWarps];
   // (no early launch of what follows: a forward kernel's CTAs waiting on the SMs took 7 us
   // more than starting after this one)
