@@ -529,6 +529,7 @@ fa_status bwd_mod_impl(const void* Q, const void* K, const void* V, const void* 
     // keys without queries have zero gradients (see bwd_impl)
     if (static_cast<long long>(B) * H == 0 || Nk == 0) return FA_OK;
     FA_TRY(check_key_grads(dK, dV, kb));
+    FA_TRY(check_apart({{"dK", dK, kb}, {"dV", dV, kb}}, {{"K", K, kb}, {"V", V, kb}}));
     DeviceInfo dev;
     FA_TRY(device_info(&dev));
     const fa::Problem p = make_problem(B, m.Hkv, Nq, Nk, d, scale, causal, dev);

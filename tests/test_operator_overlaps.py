@@ -180,3 +180,17 @@ def test_mod_outputs_over_other_arguments(backward, out):
         assert mod(backward, **{out: at + (size[name] - 1) // 16 * 16}), name
         assert not mod(backward, **{out: at + (size[name] + 15) // 16 * 16}), name
         assert not mod(backward, **{out: at - (size[out] + 15) // 16 * 16}), name
+
+
+@no_gpu
+def test_zeroed_key_gradients_over_keys():
+    """Without queries dK and dV are zeroed: not over K or V."""
+    def empty(**at):
+        p = {n: at.get(n, BASE + (i << 32)) for n, i in MOD.items()}
+        return refused("fa_bwd_mod", [*(p[n] for n in ("Q", "K", "V", "O", "dO", "LSE", "dQ", "dK", "dV")),
+                                      None, None, None, None, 3, 4, 2, 0, 50, 64, 0.1, 1, 0.0, None, 0,
+                                      None])
+
+    assert not empty()
+    for out, over in (("dK", "K"), ("dK", "V"), ("dV", "K"), ("dV", "V"), ("dK", "dV")):
+        assert empty(**{out: BASE + (MOD[over] << 32)})
