@@ -55,11 +55,17 @@
 //   * Modified scores (mod.cuh): kMode compiles the kernel once per combination of cap and
 //     distance bias.  A unit walks the key tiles between its first row's first and its last
 //     row's last visible key, K and V come from the query head's key head, and units of
-//     documents are dealt dearest first.  A capped score costs 5 packed operations for two
-//     entries: B=1 H=16 N=8192 d=128 causal 332 us against 270 without a cap (B=2 N=4096: 187
-//     against 145), bound, as without, by the softmax warps' instruction stream.  Where every
-//     score is near its cap the formula's two exponential-unit operations an entry make it
-//     350 (B=2 N=4096).
+//     documents are dealt dearest first (up to kMaxOrdered of them).  A capped score costs 5
+//     packed operations for two entries: B=1 H=16 N=8192 d=128 causal 326 us against 270
+//     without a cap (B=2 N=4096: 183 against 150), bound, as without, by the softmax warps'
+//     instruction stream.  (Sustained load, where the power limit holds the clock at 1.6 to 1.77
+//     GHz; bursts of a few calls at 1.97 GHz take 308, 244, 177 and 137.)  Where every score is
+//     near its cap the formula's two exponential-unit operations an entry make it 308 (B=2
+//     N=4096).
+//   * Roundings: scores, statistics and O are float32 until O's one rounding.  P goes to bf16
+//     as the second product's operand, half a step of 2^-8 on each weight, while l sums the
+//     unrounded ones: O is 0.0020 to 0.0023 off (relative 2-norm) where its own rounding alone
+//     is 0.0017.  A float32 P would need a tf32 product, at half the rate.
 #include <cfloat>
 #include <cstdint>
 

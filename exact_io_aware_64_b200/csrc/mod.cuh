@@ -64,9 +64,10 @@ struct CapArgs {
 // backward, with sech^2(sqrt(u)) to degree 2, 1.6e-4 (it multiplies dS, which is rounded to
 // bf16 next, 2^-8).  Minimax in the relative error, fitted here by iteratively reweighted
 // least squares.  The forward pays 6 % for its wider range (B=2 H=16 N=4096 d=128 causal, Q
-// and K of deviation 1.5, cap 50: 182 us against 171 with degree 3), because a tile outside
+// and K of deviation 1.5, cap 50: 183 us against 171 with degree 3), because a tile outside
 // it costs the forward more: with 1/2, scores of that size under a cap of 20 took 318 us,
-// now 183.  The backward takes 560 us either way there and 4 % less under the larger cap.
+// now 183.  The backward would gain nothing from it there (560 us either way) and lose 4 %
+// under the larger cap.
 // Caps far above the scores use no more than |y| <= 1/5, where the Taylor series of the
 // same degrees are off by 5.6e-8 (degree 3; less for 4) and 6e-4 y^2 at most: scores in the
 // hundreds then keep float32's digits.
@@ -263,8 +264,11 @@ __device__ __forceinline__ float cap_any(float s, const CapArgs& c) {
 // range: the formula for all of them, in registers, while its absolute error, 2^-23 out, is
 // far below the rounding of P (out <= 256).  Larger caps go entry by entry through a copy in
 // local memory: a rolled loop, which leaves the instruction cache to the usual path, but
-// which the small L1 beside the kernels' shared memory makes several times slower than the
-// tile's other work.
+// which the small L1 beside the kernels' shared memory makes many times slower than the
+// tile's other work (B=2 H=16 N=4096 d=128 causal, products of deviation 16: cap 100 323 us,
+// cap 1000 2068).  A third branch, the polynomial as far as it holds, takes that to 228 and
+// costs every capped call its place in the instruction cache (the prompt B=1 H=16 over 4 N=8192
+// 289 -> 313 us).
 template <int N>
 __device__ __forceinline__ void cap_scores_any(float* s, const CapArgs& c) {
   if (c.out <= 256.f) {

@@ -47,6 +47,9 @@
 // part for the joining kernel.  A single warp going through 128 columns takes longer than
 // the tile's share of the HBM rate (1.7 us against 1.5 us a tile, 2.2 us capped); 32 columns
 // each do not.
+//
+// Roundings: P goes to bf16 as the second product's operand (as in the forward kernel); pieces,
+// their statistics and the join are float32, O is rounded once.
 #include <cstdint>
 
 #include "internal.h"

@@ -325,9 +325,15 @@ FA_API fa_status fa_doc_ranges(const int* doc_ids, int* doc_start, int* doc_end,
  *   prefix  in : [B] int32 or NULL: keys below it are visible to every row of sequence b
  *                (of the same document); needs causal = 1; taken as min(prefix, Nk), and
  *                a negative one as 0
- *   doc_start, doc_end in : [B,Nk] int32 from fa_doc_ranges over the key tokens, or both NULL
+ *   doc_start, doc_end in : [B,Nk] int32 from fa_doc_ranges over the key tokens, or both NULL.
+ *                (Work over documents is dealt by cost while B times the tiles of a sequence,
+ *                256 query rows each here, 128 rows in the backward, is at most 256, and in
+ *                index order beyond: the results are the same, a long batch of uneven
+ *                documents may take some 10 % longer.)
  *   softcap: 0 (no cap), or between 1e-9 and 1e9 with scale / softcap between 1e-12 and
- *                1e12; d, scale, causal as in fa_fwd_qk.
+ *                1e12; d, scale, causal as in fa_fwd_qk.  (Tiles with a score above 0.8 of
+ *                the cap, or, from a cap of 52 on, above some 35, take up to twice as long; under
+ *                caps from 177 on more than ten times.)
  * A row that sees no key gets O = 0 and LSE = -inf.  K and V must hold finite values in
  * every row, visible or not (a hidden key's probability is zero, and 0 times a NaN is a
  * NaN).  doc_start and doc_end arrays of other origin that do not rise along the sequence
@@ -347,8 +353,9 @@ FA_API fa_status fa_fwd_mod(const void* Q, const void* K, const void* V, void* O
  *   dQ out: [B,H,Nq,d] bf16;  dK, dV out: [B,Hkv,Nk,d] bf16
  *   workspace: fa_bwd_workspace_bytes(B,H,Nq,d) bytes, 16-byte aligned
  * Every row of dQ, dK and dV is written: zeros for a row that sees no key and for a key
- * that no row sees (also when Nq == 0).  Gradients and workspace must not overlap each
- * other or an input.  Three kernels, no atomics; otherwise as fa_bwd_qk.
+ * that no row sees (also when Nq == 0).  Q, O and dO must hold finite values in every row
+ * too, whether it sees a key or not.  Gradients and workspace must not overlap each other or
+ * an input.  Three kernels, no atomics; otherwise as fa_bwd_qk.
  */
 FA_API fa_status fa_bwd_mod(const void* Q, const void* K, const void* V, const void* O,
                             const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
@@ -419,7 +426,7 @@ FA_API size_t fa_fwd_tree_workspace_bytes(int B, int H, int Hkv, int T, int d);
  *        (O, LSE and workspace must not overlap one another or any input)
  *   T <= 64; B <= 4096; page 8, 16, 32, 64 or a multiple of 128; d 64 or 128
  * A row that sees no key gets O = 0 and LSE = -inf.  Slots of a page behind its sequence's
- * end may hold anything.  A sequence whose lengths are out of range (cache_lens[b] outside
+ * end may hold anything; cached tokens, drafted ones among them, must hold finite values.  A sequence whose lengths are out of range (cache_lens[b] outside
  * [0, max_pages * page], n_b outside [0, min(T, cache_lens[b])]) is skipped, and a page
  * number outside [0, num_pages) makes that sequence's outputs wrong; both are reported by
  * fa_check_device_error as FA_ERR_INVALID_ARG.  Two kernels on `stream`, no atomics: the
