@@ -635,8 +635,8 @@ def rotary_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0,
     scale is 0.1 ln(factor) + 1.  Returns (inv_freq, mscale)."""
     if rot < 2 or rot % 2:
         raise ValueError("rot must be even and positive")
-    if not factor > 0 or not base > 0:
-        raise ValueError("base and factor must be positive")
+    if not (0 < factor < math.inf and 0 < base < math.inf and 0 < original_len < math.inf):
+        raise ValueError("base, factor and original_len must be positive and finite")
     k = torch.arange(rot // 2, dtype=torch.float64)
     mscale = 1.0
     if scaling == "linear":
