@@ -610,14 +610,28 @@ View flat_view(const void* p, size_t bytes) {
 // Whether two views may share a byte.  They do not if they lie apart, or if their rows,
 // taken modulo a stride, do: heads of one fused buffer lie apart modulo its token stride,
 // slices of a head-major one modulo its batch stride.
-bool may_share(const View& x, const View& y) {
+bool may_share(View x, View y) {
+  if (!overlaps(x.p, x.span(), y.p, y.span())) return false;
+  const long long off = static_cast<const char*>(y.p) - static_cast<const char*>(x.p);
+  // a common stride that steps past all that both views cover without it (a pitch between
+  // sequences): only equal indices can meet, so one of them stands for all
+  for (int pass = 0; pass < 3; ++pass) {
+    for (int k = 0; k < 3; ++k) {
+      if (x.n[k] <= 1 || y.n[k] <= 1 || x.st[k] != y.st[k]) continue;
+      const long long nx = x.n[k], ny = y.n[k];
+      x.n[k] = y.n[k] = 1;
+      const long long first = off < 0 ? off : 0;
+      const long long last = x.span() > off + y.span() ? x.span() : off + y.span();
+      if (last - first > x.st[k]) x.n[k] = nx, y.n[k] = ny;
+    }
+  }
   if (!overlaps(x.p, x.span(), y.p, y.span())) return false;
   for (const View* v : {&x, &y}) {
     for (int k = 0; k < 3; ++k) {
       const long long period = v->st[k];
       if (v->n[k] <= 1 || period <= 0) continue;
       const long long nx = x.span_within(period), ny = y.span_within(period);
-      long long at = (static_cast<const char*>(y.p) - static_cast<const char*>(x.p)) % period;
+      long long at = off % period;
       if (at < 0) at += period;
       if (at >= nx && at + ny <= period) return false;
     }

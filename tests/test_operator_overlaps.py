@@ -2,6 +2,7 @@
 accepted call gets as far as asking for a device)."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -63,6 +64,13 @@ def test_rotary_layouts_that_share_nothing(elem):
     # head-major: [B, heads, N, d] of both, one after the other in every sequence
     q, k = View(0, 0, 6 * 640, 640, 64), View(0, 4 * 640, 6 * 640, 640, 64)
     assert not rotary(q, q, k, k, **kw)
+    # the same with a pitch between sequences that is no multiple of a token's
+    q, k = View(0, 0, 10 * 512 + 72, 64, 512), View(0, 256, 10 * 512 + 72, 64, 512)
+    assert not rotary(q, q, k, k, **kw)
+    assert not rotary(q, q, k, dense(1, 2), **kw)
+    # and one between heads of tokens side by side: [B, heads, N, 2, d]
+    q, k = View(0, 0, 5 * 1288, 1288, 128), View(0, 64, 5 * 1288, 1288, 128)
+    assert not rotary(q, q, k, k, H=4, Hkv=4, **kw)
     # one token in place: the token's own stride says nothing
     assert not rotary(dense(0, 4, N=1), View(0, 0, 256, 64, 9999), dense(1, 2, N=1), dense(2, 2, N=1),
                       N=1, **kw)
@@ -83,6 +91,9 @@ def test_rotary_outputs_over_other_arguments(elem):
     # heads that both tensors have, in place: turned twice
     assert rotary(f, f, fused(0, 3, 8), fused(0, 3, 8), **kw)
     assert rotary(x, x, View(0, 640, *x.st), View(0, 640, *x.st), **kw)
+    p = View(0, 0, 10 * 512 + 72, 64, 512)
+    assert rotary(p, p, View(0, 192, *p.st), View(0, 192, *p.st), **kw)
+    assert rotary(p, p, View(0, 512, *p.st), View(0, 512, *p.st), **kw)
     # outputs with heads in common
     assert rotary(dense(0, 4), fused(2, 0, 8), dense(1, 2), fused(2, 3, 8), **kw)
     assert rotary(dense(0, 4), dense(2, 4), dense(1, 2), dense(2, 2, at=100), **kw)
@@ -98,6 +109,40 @@ def test_rotary_output_rows_that_share_elements():
         assert rotary(q, View(1, 0, *st), k, dense(3, 2))
     for st in ((2560, 640, 64), (64, 640, 2560 * 8), (64, 128, 512), (1 << 30, 640, 64)):
         assert not rotary(q, View(1, 0, *st), k, dense(3, 2))
+
+
+def elements(v, heads, B, N, d):
+    b, h, n, e = np.ogrid[:B, :heads, :N, :d]
+    return (v.at + b * v.st[0] + h * v.st[1] + n * v.st[2] + e).ravel()
+
+
+@no_gpu
+def test_rotary_views_against_their_elements():
+    """Random small views of one buffer: what shares an element is always refused, and what
+    is laid out as one of the usual permutations of (batch, head, token) mostly is not."""
+    rng = np.random.default_rng(1)
+    accepted = apart = 0
+    for _ in range(3000):
+        B, H, Hkv, N, d = (int(rng.integers(1, m)) for m in (4, 5, 4, 6, 7))
+        d += d % 2
+        total, pad = H + Hkv + int(rng.integers(0, 3)), [int(x) for x in rng.integers(0, 3, 3)]
+        order = rng.permutation(3)  # the dimensions from the innermost out
+        st, step = [0, 0, 0], d + pad[0]
+        for k, p in zip(order, (*pad[1:], 0)):
+            st[k] = step
+            step = step * (B, total, N)[k] + p
+        if rng.random() < 0.2:
+            st[int(rng.integers(0, 3))] = int(rng.integers(0, 2 * d))
+        q = View(0, 16, *st)
+        k = View(0, 16 + int(rng.choice([H * st[1], st[1], int(rng.integers(-12, 60))])), *st)
+        out = [elements(q, H, B, N, d), elements(k, Hkv, B, N, d)]
+        shares = (len(np.unique(out[0])) < out[0].size or len(np.unique(out[1])) < out[1].size or
+                  np.intersect1d(*out).size > 0)
+        got = rotary(q, q, k, k, B=B, H=H, Hkv=Hkv, N=N, d=d)
+        assert got or not shares, (B, H, Hkv, N, d, st, k.at)
+        apart += not shares
+        accepted += not got
+    assert accepted > 0.9 * apart > 500, (accepted, apart)
 
 
 @no_gpu
